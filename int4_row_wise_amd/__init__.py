@@ -5,6 +5,9 @@ The compute lives in a HIP C-ABI library (``libqemb.so``, declared in
 over it that only marshals torch tensors and the current stream.  The
 library loads on first use and raises if it was not built; there is no CPU
 fallback.  :mod:`int4_row_wise_amd.synth` draws the seeded synthetic inputs.
+:mod:`int4_row_wise_amd.attention` binds ``libqemb_attention.so``
+(``include/qemb_attention.h``): attention over a paged key-value cache of
+16-bit or packed INT8 / INT4 rows.
 """
 from .qemb import (  # noqa: F401
     RANGE, GREEDY, SUM, WEIGHTED_SUM, CODEBOOK_ITERS, SYMMETRIC, PERCENTILE, ACIQ, QembError,
@@ -14,4 +17,7 @@ from .qemb import (  # noqa: F401
     l2_error_codebook, load_library, quantize_codebook, quantize_rowwise, row_stride,
     COMPRESS_VERBATIM, compress_bound, compress_pooled, compress_record_bytes, compress_workspace_bytes,
     decompress_pooled, compress_pooled_noalloc, COMPRESS_NOALLOC_MAX_VECTORS,
+)
+from .attention import (  # noqa: F401
+    decode_attention, decode_workspace_bytes, evict, load_attention_library, norm_rope, prompt_attention,
 )

@@ -1,4 +1,5 @@
-"""Build libqemb.so (the HIP C-ABI library) in-tree for gfx950.
+"""Build libqemb.so and libqemb_attention.so (the HIP C-ABI libraries) in-tree
+for gfx950.
 
     python -m int4_row_wise_amd.build
 
@@ -22,6 +23,11 @@ LIB_HASH = LIB + ".srchash"  # source sha256 recorded at build time
 # the gather floor (a measurement aid for bench.py, not part of the C ABI)
 FLOOR_SRC = os.path.join(CSRC, "gather_floor.hip")
 FLOOR_LIB = os.path.join(HERE, "libqemb_floor.so")
+# attention over a paged key-value cache: a translation unit and library of its own
+ATTN_DIR = os.path.join(CSRC, "attention")
+ATTN_SRC = os.path.join(ATTN_DIR, "attention.hip")
+ATTN_HEADER = os.path.join(ROOT, "include", "qemb_attention.h")
+ATTN_LIB = os.path.join(HERE, "libqemb_attention.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
@@ -37,33 +43,61 @@ def hipcc() -> str:
     return "hipcc"
 
 
+def _compile(src: str, lib: str) -> tuple:
+    """Start hipcc on one translation unit: (process, temporary output, library)."""
+    tmp = lib + ".tmp%d" % os.getpid()
+    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, src]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp, lib
+
+
+def _finish(job: tuple, verbose: bool) -> None:
+    proc, tmp, lib = job
+    out, _ = proc.communicate()
+    out = "\n".join(l for l in out.splitlines() if "packed-fp32-ops" not in l)
+    if proc.returncode != 0:
+        raise RuntimeError("hipcc failed:\n" + out)
+    if out.strip() and verbose:
+        print(out)
+    os.replace(tmp, lib)
+
+
+def _record(lib: str, sha: str) -> None:
+    with open(lib + ".srchash", "w") as f:
+        f.write(sha + "\n")
+
+
+def _newer(lib: str, sources: list) -> bool:
+    return os.path.exists(lib) and os.path.getmtime(lib) >= max(os.path.getmtime(f) for f in sources)
+
+
+def build_attention(verbose: bool = False) -> str:
+    """Compile csrc/attention/attention.hip into libqemb_attention.so."""
+    sha = attention_source_sha256()
+    _finish(_compile(ATTN_SRC, ATTN_LIB), verbose)
+    _record(ATTN_LIB, sha)
+    return ATTN_LIB
+
+
 def build(force: bool = True, verbose: bool = False) -> str:
-    """Compile csrc/qemb.hip into int4_row_wise_amd/libqemb.so."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= max(
-            [os.path.getmtime(f) for f in source_files()] + [os.path.getmtime(HEADER)]):
+    """Compile csrc/qemb.hip into int4_row_wise_amd/libqemb.so, and beside it
+    the gather floor and the attention library."""
+    if not force and _newer(LIB, source_files() + [HEADER]) and _newer(ATTN_LIB, attention_source_files()):
         return LIB
     # the hash of the sources as compiled: taken before the compiler reads
     # them, so an edit made while it runs cannot be recorded for this build
     src_hash = source_sha256()
-    # the floor (one small kernel) compiles beside the library
-    floor_tmp = FLOOR_LIB + ".tmp%d" % os.getpid()
-    floor = subprocess.Popen([hipcc(), *HIPCC_FLAGS, "-o", floor_tmp, FLOOR_SRC], stdout=subprocess.PIPE,
-                             stderr=subprocess.STDOUT, text=True)
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, SRC]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    floor_out, _ = floor.communicate()
-    out = "\n".join(l for l in (r.stdout + floor_out).splitlines() if "packed-fp32-ops" not in l)
-    if r.returncode != 0 or floor.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + out)
-    if out.strip() and verbose:
-        print(out)
-    os.replace(floor_tmp, FLOOR_LIB)
-    os.replace(tmp, LIB)
-    with open(LIB_HASH, "w") as f:
-        f.write(src_hash + "\n")
+    attn_hash = attention_source_sha256()
+    # the small libraries compile beside the large one
+    jobs = [_compile(FLOOR_SRC, FLOOR_LIB), _compile(ATTN_SRC, ATTN_LIB), _compile(SRC, LIB)]
+    try:
+        for job in jobs:
+            _finish(job, verbose)
+    finally:
+        for proc, _, _ in jobs:
+            if proc.poll() is None:
+                proc.kill()
+    _record(LIB, src_hash)
+    _record(ATTN_LIB, attn_hash)
     return LIB
 
 
@@ -76,9 +110,24 @@ def source_files() -> list:
 def source_sha256() -> str:
     """sha256 over the kernel sources the library is built from (each file's
     name and bytes, in sorted order)."""
+    return _sha256(source_files())
+
+
+def attention_source_files() -> list:
+    """The attention library's sources: its own, the shared helpers and the headers."""
+    own = [os.path.join(ATTN_DIR, f) for f in os.listdir(ATTN_DIR) if f.endswith((".hip", ".inc"))]
+    return sorted(own) + [os.path.join(CSRC, "common.inc"), ATTN_HEADER, HEADER]
+
+
+def attention_source_sha256() -> str:
+    """sha256 over the attention library's sources, as source_sha256."""
+    return _sha256(attention_source_files())
+
+
+def _sha256(paths: list) -> str:
     import hashlib
     h = hashlib.sha256()
-    for path in source_files():
+    for path in paths:
         h.update(os.path.basename(path).encode() + b"\0")
         with open(path, "rb") as f:
             h.update(f.read())
@@ -87,8 +136,13 @@ def source_sha256() -> str:
 
 def built_source_sha256() -> str | None:
     """The source hash recorded when libqemb.so was last built, if any."""
+    return recorded_hash(LIB)
+
+
+def recorded_hash(lib: str) -> str | None:
+    """The source hash recorded when a library was last built, if any."""
     try:
-        with open(LIB_HASH) as f:
+        with open(lib + ".srchash") as f:
             return f.read().strip()
     except OSError:
         return None
@@ -96,9 +150,11 @@ def built_source_sha256() -> str | None:
 
 def ensure_built() -> str:
     """Build only if no library exists yet (used by tests, smoke and bench)."""
-    if os.path.exists(LIB):
-        return LIB
-    return build(force=True)
+    if not os.path.exists(LIB):
+        return build(force=True)
+    if not os.path.exists(ATTN_LIB):
+        build_attention()
+    return LIB
 
 
 if __name__ == "__main__":
