@@ -120,6 +120,8 @@ int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q
                           float* lse, int32_t* err_count, qemb_stream_t stream) {
   if (q_tokens < 0 || k_tokens < 0 || batch < 0 || window < 0 || sinks < 0 || max_q < 0) return QEMB_E_INVALID_ARG;
   if (q_tokens > INT32_MAX || k_tokens > INT32_MAX) return QEMB_E_UNSUPPORTED;
+  // a tile's byte offsets are 32 bits wide
+  if (k_token_stride > kMaxTokenStride || v_token_stride > kMaxTokenStride) return QEMB_E_UNSUPPORTED;
   if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
   if (!strides_fit(q_token_stride, q_head_stride) || !strides_fit(k_token_stride, k_head_stride) ||
       !strides_fit(v_token_stride, v_head_stride))
