@@ -165,6 +165,8 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
   if (bits != 16 && bits != 8 && bits != 4) return QEMB_E_INVALID_ARG;
   if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
   if ((int64_t)width * page_size > INT32_MAX) return QEMB_E_UNSUPPORTED;
+  if ((int64_t)kv_heads * page_size > INT32_MAX || (int64_t)kv_heads * page_size * row_bytes_of(dim, bits) > INT32_MAX)
+    return QEMB_E_UNSUPPORTED;  // a page's bytes are counted in 32 bits
   if (batch == 0) return QEMB_OK;
   if (!q || !out || !seq_lens || (width > 0 && !block_table) || (pages > 0 && (!k_pages || !v_pages)))
     return QEMB_E_INVALID_ARG;
