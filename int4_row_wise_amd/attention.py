@@ -19,7 +19,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .qemb import INDEX_INT32, INDEX_INT64, QembError, _dev, _ptr, _stream
+from .qemb import INDEX_INT32, INDEX_INT64, QembError, _ptr
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqemb_attention.so")
@@ -75,45 +75,66 @@ def _check(fn: str, rc: int) -> None:
         raise QembError(fn, rc, _REASONS.get(rc, "unknown error"))
 
 
-def _heads(name: str, t: torch.Tensor, dtype=None) -> None:
-    """A [tokens, heads, dim] tensor whose last dimension is contiguous."""
+# The current stream's handle by device index, without building a Stream object
+# (1.9 us of a call that takes about ten).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _device(name: str, t: torch.Tensor) -> int:
+    """The GPU index of the tensor that decides where a call runs."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError("%s must be [tokens, heads, dim] with dim contiguous" % name)
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        raise TypeError("%s must be %s, got %s" % (name, dtype or "bfloat16 or float16", t.dtype))
+    return t.get_device()
 
 
-def _exact(name: str, t: Optional[torch.Tensor], shape: tuple, dtype) -> None:
-    """An optional contiguous tensor of a given shape and type."""
-    if t is None:
+def _want(name: str, t: torch.Tensor, shape: tuple, dtype, dev: int) -> None:
+    """A contiguous tensor of a given shape and type on a given GPU."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
         return
-    _dev(name, t, dtype)
-    if tuple(t.shape) != shape:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
+    raise ValueError("%s must be contiguous" % name)
 
 
-def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError("all tensors must be on %s, got one on %s" % (first.device, t.device))
+def _heads(name: str, t: torch.Tensor, dtype, dev: int) -> tuple:
+    """A [tokens, heads, dim] tensor whose last dimension is contiguous: its strides."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise TypeError("%s must be a CUDA (HIP) tensor on cuda:%d" % (name, dev))
+    if t.dtype is not dtype or dtype not in _DTYPES:
+        raise TypeError("%s must be %s, got %s" % (name, dtype if dtype in _DTYPES else "bfloat16 or float16", t.dtype))
+    stride = t.stride()
+    if len(stride) != 3 or (stride[2] != 1 and t.shape[2] > 1):
+        raise ValueError("%s must be [tokens, heads, dim] with dim contiguous" % name)
+    return stride
 
 
-def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int, bits: int, dtype) -> Tuple[int, int, int]:
+def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int, bits: int, dtype, dev: int) -> tuple:
     """(pages, kv heads, page size) of a cache of rows of `dim` elements."""
-    if bits not in (16, 8, 4):
+    if bits == 16:
+        row = dim
+    elif bits == 8 or bits == 4:
+        row, dtype = (dim * bits // 8 + 4 + 15) // 16 * 16, torch.uint8
+    else:
         raise ValueError("bits must be 16, 8 or 4")
-    kind = dtype if bits == 16 else torch.uint8
-    row = dim if bits == 16 else (dim * bits // 8 + 4 + 15) // 16 * 16
-    _dev("k_pages", k_pages, kind)
-    _dev("v_pages", v_pages, kind)
-    if k_pages.dim() != 4 or k_pages.shape[3] != row or k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages must both be [pages, kv_heads, page_size, %d]" % row)
-    pages, heads, size, _ = k_pages.shape
+    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
+        raise TypeError("k_pages must be a CUDA (HIP) tensor")
+    shape = k_pages.shape
+    if len(shape) != 4 or shape[3] != row:
+        raise ValueError("k_pages must be [pages, kv_heads, page_size, %d], got %s" % (row, list(shape)))
+    size = shape[2]
     if size < 1 or size & (size - 1):
         raise ValueError("page_size must be a power of two, got %d" % size)
-    return pages, heads, size
+    _want("k_pages", k_pages, shape, dtype, dev)
+    _want("v_pages", v_pages, shape, dtype, dev)
+    return shape[0], shape[1], size
 
 
 def norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
@@ -129,46 +150,50 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin
     written to the flat `slots` [N] int64 (page * page_size + offset; negative:
     not written).  Returns (q_out, k_out); k_out is None with pages unless it is
     given."""
-    _heads("q", q)
-    _heads("k", k, q.dtype)
+    dev, dtype = _device("q", q), q.dtype
+    qs, ks, vs = _heads("q", q, dtype, dev), _heads("k", k, dtype, dev), (0, 0)
     n, hq, d = q.shape
     hkv = k.shape[1]
     if k.shape[0] != n or k.shape[2] != d:
         raise ValueError("q and k must have the same tokens and head dim")
-    _exact("positions", positions, (n,), positions.dtype)
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise TypeError("positions must be int32 or int64")
-    _dev("cos_sin", cos_sin, torch.float32)
-    if cos_sin.dim() != 2:
+    wide = isinstance(positions, torch.Tensor) and positions.dtype is torch.int64
+    _want("positions", positions, (n,), torch.int64 if wide else torch.int32, dev)
+    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [places, rot_dim]")
-    _exact("q_weight", q_weight, (d,), q.dtype)
-    _exact("k_weight", k_weight, (d,), q.dtype)
+    places, rot = cos_sin.shape
+    _want("cos_sin", cos_sin, (places, rot), torch.float32, dev)
+    if q_weight is not None:
+        _want("q_weight", q_weight, (d,), dtype, dev)
+    if k_weight is not None:
+        _want("k_weight", k_weight, (d,), dtype, dev)
     pages = size = 0
-    if (k_pages is None) != (v_pages is None) or (k_pages is None) != (slots is None) or (k_pages is None) != (v is None):
-        raise ValueError("v, k_pages, v_pages and slots come together")
     if k_pages is not None:
-        _heads("v", v, q.dtype)
+        if v_pages is None or slots is None or v is None:
+            raise ValueError("v, k_pages, v_pages and slots come together")
+        vs = _heads("v", v, dtype, dev)
         if v.shape != k.shape:
             raise ValueError("v must have k's shape")
-        pages, heads, size = _cache(k_pages, v_pages, d, bits, q.dtype)
+        pages, heads, size = _cache(k_pages, v_pages, d, bits, dtype, dev)
         if heads != hkv:
             raise ValueError("the cache has %d kv heads, k has %d" % (heads, hkv))
-        _exact("slots", slots, (n,), torch.int64)
+        _want("slots", slots, (n,), torch.int64, dev)
+    elif v_pages is not None or slots is not None or v is not None:
+        raise ValueError("v, k_pages, v_pages and slots come together")
     elif k_out is None:
-        k_out = torch.empty((n, hkv, d), dtype=q.dtype, device=q.device)
+        k_out = torch.empty((n, hkv, d), dtype=dtype, device=q.device)
     if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-    _exact("q_out", q_out, (n, hq, d), q.dtype)
-    _exact("k_out", k_out, (n, hkv, d), q.dtype)
-    _exact("err_count", err_count, (1,), torch.int32)
-    _same_device(q, k, v, positions, cos_sin, q_weight, k_weight, k_pages, v_pages, slots, q_out, k_out, err_count)
-    vt, vh = (v.stride(0), v.stride(1)) if v is not None else (0, 0)
+        q_out = torch.empty((n, hq, d), dtype=dtype, device=q.device)
+    else:
+        _want("q_out", q_out, (n, hq, d), dtype, dev)
+    if k_out is not None:
+        _want("k_out", k_out, (n, hkv, d), dtype, dev)
+    if err_count is not None:
+        _want("err_count", err_count, (1,), torch.int32, dev)
     _check("qemb_norm_rope", load_attention_library().qemb_norm_rope(
-        q.data_ptr(), k.data_ptr(), _ptr(v), n, hq, hkv, d, _DTYPES[q.dtype], q.stride(0), q.stride(1), k.stride(0),
-        k.stride(1), vt, vh, positions.data_ptr(), INDEX_INT64 if positions.dtype == torch.int64 else INDEX_INT32,
-        cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved), _ptr(q_weight), _ptr(k_weight), eps,
-        q_out.data_ptr(), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(slots), pages, size, bits, _ptr(err_count),
-        _stream(q)))
+        q.data_ptr(), k.data_ptr(), _ptr(v), n, hq, hkv, d, _DTYPES[dtype], qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+        positions.data_ptr(), INDEX_INT64 if wide else INDEX_INT32, cos_sin.data_ptr(), places, rot, int(interleaved),
+        _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(slots),
+        pages, size, bits, _ptr(err_count), _raw_stream(dev)))
     return q_out, k_out
 
 
@@ -183,28 +208,28 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offset
     `sinks` keys.  max_q (the longest run of queries) only shapes the grid.
     scale: 1 / sqrt(d) unless given.  Returns out [Nq, Hq, d]; lse [Nq, Hq]
     float32 is filled if given."""
-    _heads("q", q)
-    _heads("k", k, q.dtype)
-    _heads("v", v, q.dtype)
+    dev, dtype = _device("q", q), q.dtype
+    qs, ks, vs = _heads("q", q, dtype, dev), _heads("k", k, dtype, dev), _heads("v", v, dtype, dev)
     n, hq, d = q.shape
     if k.shape != v.shape or k.shape[2] != d:
         raise ValueError("k and v must be [tokens, kv_heads, %d] alike" % d)
-    batch = q_offsets.numel() - 1
-    if batch < 0:
+    if not isinstance(q_offsets, torch.Tensor) or q_offsets.numel() < 1:
         raise ValueError("q_offsets must have batch + 1 entries")
-    _exact("q_offsets", q_offsets, (batch + 1,), torch.int32)
-    _exact("k_offsets", k_offsets, (batch + 1,), torch.int32)
+    batch = q_offsets.numel() - 1
+    _want("q_offsets", q_offsets, (batch + 1,), torch.int32, dev)
+    _want("k_offsets", k_offsets, (batch + 1,), torch.int32, dev)
     if out is None:
-        out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-    _exact("out", out, (n, hq, d), q.dtype)
-    _exact("lse", lse, (n, hq), torch.float32)
-    _exact("err_count", err_count, (1,), torch.int32)
-    _same_device(q, k, v, q_offsets, k_offsets, out, lse, err_count)
+        out = torch.empty((n, hq, d), dtype=dtype, device=q.device)
+    else:
+        _want("out", out, (n, hq, d), dtype, dev)
+    if lse is not None:
+        _want("lse", lse, (n, hq), torch.float32, dev)
+    if err_count is not None:
+        _want("err_count", err_count, (1,), torch.int32, dev)
     _check("qemb_prompt_attention", load_attention_library().qemb_prompt_attention(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), n, k.shape[0], batch, hq, k.shape[1], d, _DTYPES[q.dtype], q.stride(0),
-        q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1), q_offsets.data_ptr(), k_offsets.data_ptr(),
-        max_q, window, sinks, d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse), _ptr(err_count),
-        _stream(q)))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), n, k.shape[0], batch, hq, k.shape[1], d, _DTYPES[dtype], qs[0], qs[1],
+        ks[0], ks[1], vs[0], vs[1], q_offsets.data_ptr(), k_offsets.data_ptr(), max_q, window, sinks,
+        d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse), _ptr(err_count), _raw_stream(dev)))
     return out
 
 
@@ -227,38 +252,40 @@ def decode_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     float32 (M >= every length) grows by each key's softmax weight, summed over
     the query heads of its kv head.  Returns out [B, Hq, d]; lse [B, Hq] float32
     is filled if given."""
-    _dev("q", q)
-    if q.dim() != 3 or q.dtype not in _DTYPES:
-        raise TypeError("q must be [batch, heads, dim] of bfloat16 or float16")
+    dev, dtype = _device("q", q), q.dtype
+    if q.dim() != 3 or dtype not in _DTYPES or not q.is_contiguous():
+        raise TypeError("q must be [batch, heads, dim] of bfloat16 or float16, contiguous")
     b, hq, d = q.shape
-    pages, hkv, size = _cache(k_pages, v_pages, d, bits, q.dtype)
-    _dev("block_table", block_table, torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != b:
+    pages, hkv, size = _cache(k_pages, v_pages, d, bits, dtype, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [%d, width]" % b)
-    _exact("seq_lens", seq_lens, (b,), torch.int32)
+    width = block_table.shape[1]
+    _want("block_table", block_table, (b, width), torch.int32, dev)
+    _want("seq_lens", seq_lens, (b,), torch.int32, dev)
     mass_len = 0
     if mass is not None:
         mass_len = mass.shape[-1]
-        _exact("mass", mass, (b, hkv, mass_len), torch.float32)
+        _want("mass", mass, (b, hkv, mass_len), torch.float32, dev)
     if out is None:
-        out = torch.empty((b, hq, d), dtype=q.dtype, device=q.device)
-    _exact("out", out, (b, hq, d), q.dtype)
-    _exact("lse", lse, (b, hq), torch.float32)
-    _exact("err_count", err_count, (1,), torch.int32)
-    L = load_attention_library()
-    width = block_table.shape[1]
-    need = int(L.qemb_decode_workspace_bytes(b, hq, hkv, d, width, size, window, sinks, mass is not None))
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        out = torch.empty((b, hq, d), dtype=dtype, device=q.device)
     else:
-        _dev("workspace", workspace, torch.uint8)
+        _want("out", out, (b, hq, d), dtype, dev)
+    if lse is not None:
+        _want("lse", lse, (b, hq), torch.float32, dev)
+    if err_count is not None:
+        _want("err_count", err_count, (1,), torch.int32, dev)
+    L = load_attention_library()
+    need = L.qemb_decode_workspace_bytes(b, hq, hkv, d, width, size, window, sinks, mass is not None)
+    if workspace is not None:
         if workspace.numel() < need:
             raise ValueError("workspace must have at least %d bytes" % need)
-    _same_device(q, k_pages, v_pages, block_table, seq_lens, mass, out, lse, workspace, err_count)
+        _want("workspace", workspace, workspace.shape, torch.uint8, dev)
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _check("qemb_decode_attention", L.qemb_decode_attention(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages, size, bits, b, hq, hkv, d, _DTYPES[q.dtype],
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages, size, bits, b, hq, hkv, d, _DTYPES[dtype],
         block_table.data_ptr(), width, seq_lens.data_ptr(), window, sinks, d ** -0.5 if scale is None else scale,
-        _ptr(mass), mass_len, out.data_ptr(), _ptr(lse), _ptr(workspace), _ptr(err_count), _stream(q)))
+        _ptr(mass), mass_len, out.data_ptr(), _ptr(lse), _ptr(workspace), _ptr(err_count), _raw_stream(dev)))
     return out
 
 
@@ -273,44 +300,50 @@ def evict(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tenso
     new_k_pages / new_v_pages that overlap none of the old ones; the arrays may
     be the same).  Returns (kept [B, Hkv, keep] int32 with -1 past the end,
     new_mass [B, Hkv, >= keep], new_lens [B])."""
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages), ("new_k_pages", new_k_pages), ("new_v_pages", new_v_pages)):
-        _dev(name, t, k_pages.dtype)
-        if t.dim() != 4 or t.shape[1:] != k_pages.shape[1:]:
-            raise ValueError("%s must be [pages, kv_heads, page_size, row] like k_pages" % name)
-    if v_pages.shape != k_pages.shape or new_v_pages.shape != new_k_pages.shape:
-        raise ValueError("key and value pages must have the same shape")
+    dev = _device("k_pages", k_pages)
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [pages, kv_heads, page_size, row]")
+    kind = k_pages.dtype
     pages, hkv, size, row = k_pages.shape
     if size < 1 or size & (size - 1):
         raise ValueError("page_size must be a power of two, got %d" % size)
-    _dev("seq_lens", seq_lens, torch.int32)
+    _want("k_pages", k_pages, k_pages.shape, kind, dev)
+    _want("v_pages", v_pages, k_pages.shape, kind, dev)
+    if not isinstance(new_k_pages, torch.Tensor) or new_k_pages.dim() != 4:
+        raise ValueError("new_k_pages must be [pages, kv_heads, page_size, row] like k_pages")
+    new_pages = new_k_pages.shape[0]
+    _want("new_k_pages", new_k_pages, (new_pages, hkv, size, row), kind, dev)
+    _want("new_v_pages", new_v_pages, (new_pages, hkv, size, row), kind, dev)
     b = seq_lens.numel()
-    _dev("block_table", block_table, torch.int32)
-    _dev("new_block_table", new_block_table, torch.int32)
-    if block_table.dim() != 2 or new_block_table.dim() != 2 or block_table.shape[0] != b or new_block_table.shape[0] != b:
-        raise ValueError("block tables must be [%d, width]" % b)
-    _dev("mass", mass, torch.float32)
-    if mass.dim() != 3 or mass.shape[0] != b or mass.shape[1] != hkv:
-        raise ValueError("mass must be [%d, %d, slots]" % (b, hkv))
-    if keep < 1 or sinks < 0 or recent < 0 or sinks + recent > keep or new_block_table.shape[1] * size < keep:
+    _want("seq_lens", seq_lens, (b,), torch.int32, dev)
+    if block_table.dim() != 2 or new_block_table.dim() != 2 or mass.dim() != 3:
+        raise ValueError("block tables must be [%d, width], mass [%d, %d, slots]" % (b, b, hkv))
+    width, new_width, mass_len = block_table.shape[1], new_block_table.shape[1], mass.shape[2]
+    _want("block_table", block_table, (b, width), torch.int32, dev)
+    _want("new_block_table", new_block_table, (b, new_width), torch.int32, dev)
+    _want("mass", mass, (b, hkv, mass_len), torch.float32, dev)
+    if keep < 1 or sinks < 0 or recent < 0 or sinks + recent > keep or new_width * size < keep:
         raise ValueError("keep must be at least 1 and sinks + recent, and fit the new pages")
     if kept is None:
         kept = torch.empty((b, hkv, keep), dtype=torch.int32, device=mass.device)
+    else:
+        _want("kept", kept, (b, hkv, keep), torch.int32, dev)
     if new_mass is None:
         new_mass = torch.empty((b, hkv, keep), dtype=torch.float32, device=mass.device)
+    else:
+        if new_mass.dim() != 3 or new_mass.shape[2] < keep:
+            raise ValueError("new_mass must be [%d, %d, >= %d]" % (b, hkv, keep))
+        _want("new_mass", new_mass, (b, hkv, new_mass.shape[2]), torch.float32, dev)
     if new_lens is None:
         new_lens = torch.empty(b, dtype=torch.int32, device=mass.device)
-    _exact("kept", kept, (b, hkv, keep), torch.int32)
-    if new_mass.dim() != 3 or new_mass.shape[2] < keep:
-        raise ValueError("new_mass must be [%d, %d, >= %d]" % (b, hkv, keep))
-    _exact("new_mass", new_mass, (b, hkv, new_mass.shape[2]), torch.float32)
-    _exact("new_lens", new_lens, (b,), torch.int32)
-    _exact("err_count", err_count, (1,), torch.int32)
-    _same_device(k_pages, v_pages, block_table, seq_lens, mass, new_k_pages, new_v_pages, new_block_table, kept,
-                 new_mass, new_lens, err_count)
+    else:
+        _want("new_lens", new_lens, (b,), torch.int32, dev)
+    if err_count is not None:
+        _want("err_count", err_count, (1,), torch.int32, dev)
     _check("qemb_evict", load_attention_library().qemb_evict(
         k_pages.data_ptr(), v_pages.data_ptr(), pages, size, row * k_pages.element_size(), b, hkv,
-        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), mass.data_ptr(), mass.shape[2], keep, sinks,
-        recent, new_k_pages.data_ptr(), new_v_pages.data_ptr(), new_k_pages.shape[0], new_block_table.data_ptr(),
-        new_block_table.shape[1], kept.data_ptr(), new_mass.data_ptr(), new_mass.shape[2], new_lens.data_ptr(),
-        _ptr(err_count), _stream(k_pages)))
+        block_table.data_ptr(), width, seq_lens.data_ptr(), mass.data_ptr(), mass_len, keep, sinks,
+        recent, new_k_pages.data_ptr(), new_v_pages.data_ptr(), new_pages, new_block_table.data_ptr(),
+        new_width, kept.data_ptr(), new_mass.data_ptr(), new_mass.shape[2], new_lens.data_ptr(),
+        _ptr(err_count), _raw_stream(dev)))
     return kept, new_mass, new_lens
