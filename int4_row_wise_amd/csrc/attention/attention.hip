@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kWave = 64;
 constexpr int kBlock = 256;
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;  // of kBlock threads: a launch counts threads in 32 bits
 
 #include "../common.inc"
 #include "rows.inc"

@@ -670,3 +670,75 @@ def test_captured_step_replays(q):
             assert torch.equal(a, w), rep
         for a, w in zip(pool + new, e_pool + e_new):
             assert torch.equal(a, w), rep
+
+
+# ---- nothing to do, and refusals ----
+
+def test_empty_calls(q):
+    import torch
+    bf, i32, dev = torch.bfloat16, torch.int32, "cuda"
+
+    def empty(*shape, dtype=bf):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+    off = torch.zeros(1, dtype=i32, device=dev)
+    table = empty(0, 64, dtype=torch.float32)
+    out, k_out = q.norm_rope(empty(0, 4, 64), empty(0, 2, 64), empty(0, dtype=i32), table)
+    assert out.shape == (0, 4, 64) and k_out.shape == (0, 2, 64)
+    assert q.prompt_attention(empty(0, 4, 64), empty(0, 2, 64), empty(0, 2, 64), off, off).shape == (0, 4, 64)
+    pages = empty(0, 2, 16, 64)
+    assert q.decode_attention(empty(0, 4, 64), pages, pages, empty(0, 3, dtype=i32), empty(0, dtype=i32)).shape == (0, 4, 64)
+    # a batch whose caches are all empty, with no page at all
+    lse = torch.ones((2, 4), device=dev)
+    lens = torch.zeros(2, dtype=i32, device=dev)
+    out = q.decode_attention(torch.ones((2, 4, 64), dtype=bf, device=dev), pages, pages, empty(2, 0, dtype=i32), lens, lse=lse)
+    assert (f64(out) == 0).all() and (f64(lse) == -np.inf).all()
+    err = torch.zeros(1, dtype=i32, device=dev)
+    out = q.decode_attention(torch.ones((2, 4, 64), dtype=bf, device=dev), pages, pages, torch.zeros((2, 1), dtype=i32, device=dev),
+                             lens + 5, err_count=err)
+    assert (f64(out) == 0).all() and int(err[0]) >= 2
+    kept, mass, n = q.evict(pages, pages, empty(0, 1, dtype=i32), empty(0, dtype=i32), empty(0, 2, 16, dtype=torch.float32), 4, pages, pages,
+                            empty(0, 1, dtype=i32))
+    assert kept.shape == (0, 2, 4) and mass.shape == (0, 2, 4) and n.shape == (0,)
+
+
+def test_refusals(q):
+    import torch
+    dev, i32 = "cuda", torch.int32
+    x = torch.zeros((4, 2, 64), dtype=torch.bfloat16, device=dev)
+    pos = torch.zeros(4, dtype=i32, device=dev)
+    cs = torch.zeros((8, 64), device=dev)
+    off = torch.tensor([0, 4], dtype=i32, device=dev)
+    pages = torch.zeros((3, 2, 16, 64), dtype=torch.bfloat16, device=dev)
+    table = torch.zeros((4, 1), dtype=i32, device=dev)
+    lens = torch.ones(4, dtype=i32, device=dev)
+    mass = torch.zeros((4, 2, 16), device=dev)
+    cases = [
+        (TypeError, lambda: q.norm_rope(x.float(), x, pos, cs)),
+        (TypeError, lambda: q.norm_rope(x, x.half(), pos, cs)),
+        (TypeError, lambda: q.norm_rope(x, x, pos.short(), cs)),
+        (ValueError, lambda: q.norm_rope(x, x[:2], pos, cs)),
+        (ValueError, lambda: q.norm_rope(x.transpose(1, 2), x.transpose(1, 2), pos, cs)),
+        (ValueError, lambda: q.norm_rope(x, x, pos, cs, v=x)),
+        (ValueError, lambda: q.norm_rope(x, x, pos, cs, v=x, k_pages=pages, v_pages=pages, slots=pos.long(), bits=2)),
+        (ValueError, lambda: q.norm_rope(x, x, pos, cs, v=x, k_pages=pages, v_pages=pages, slots=pos.long(), bits=8)),
+        (q.QembError, lambda: q.norm_rope(x, x, pos, cs[:, :24].contiguous())),
+        (TypeError, lambda: q.prompt_attention(x, x, x, off.long(), off.long())),
+        (ValueError, lambda: q.prompt_attention(x, x, x[:3], off, off)),
+        (q.QembError, lambda: q.prompt_attention(x, x, x, off, off, window=-1)),
+        (TypeError, lambda: q.prompt_attention(x, x, x, off, off, lse=torch.zeros((4, 2), dtype=torch.float64, device=dev))),
+        (ValueError, lambda: q.decode_attention(x, pages[:, :, :15], pages[:, :, :15], table, lens)),
+        (ValueError, lambda: q.decode_attention(x, pages, pages, table[:2], lens)),
+        (ValueError, lambda: q.decode_attention(x, pages, pages, table, lens, mass=mass[:, :1].contiguous())),
+        (ValueError, lambda: q.decode_attention(x, pages, pages, table, lens, mass=mass, workspace=torch.zeros(4, dtype=torch.uint8, device=dev))),
+        (TypeError, lambda: q.decode_attention(x, pages, pages, table.long(), lens)),
+        (ValueError, lambda: q.decode_attention(x, pages.transpose(1, 2), pages.transpose(1, 2), table, lens)),
+        (ValueError, lambda: q.evict(pages, pages, table, lens, mass, 17, pages, pages, table)),
+        (ValueError, lambda: q.evict(pages, pages, table, lens, mass, 4, pages, pages, table, sinks=3, recent=2)),
+        (ValueError, lambda: q.evict(pages, pages, table, lens, mass, 4, pages[:, :1].contiguous(), pages, table)),
+        (TypeError, lambda: q.evict(pages, pages, table, lens, mass.double(), 4, pages, pages, table)),
+    ]
+    for i, (error, call) in enumerate(cases):
+        with pytest.raises(error):
+            call()
+            print("case %d was taken" % i)
