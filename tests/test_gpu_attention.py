@@ -742,3 +742,47 @@ def test_refusals(q):
         with pytest.raises(error):
             call()
             print("case %d was taken" % i)
+
+
+def test_own_workspace(q):
+    """A caller's workspace, whatever it holds, gives the result of the library's own."""
+    import torch
+    g = np.random.default_rng(1300)
+    cache = Cache(g, q, [3000, 700], 2, 64, 8, 16, "bf16")
+    qt, _ = rand16(g, (2, 8, 64), "bf16")
+    args = (qt, cache.pool[0], cache.pool[1], cache.table, cache.seq_lens)
+    m0, m1 = (torch.zeros((2, 2, 3000), device="cuda") for _ in range(2))
+    want = q.decode_attention(*args, bits=8, mass=m0)
+    n = q.decode_workspace_bytes(2, 8, 2, 64, cache.width, 16, with_mass=True)
+    ws = torch.full((n + 16,), 0xff, dtype=torch.uint8, device="cuda")
+    assert torch.equal(q.decode_attention(*args, bits=8, mass=m1, workspace=ws[:n]), want) and torch.equal(m0, m1)
+    assert bool((ws[n:] == 0xff).all())
+
+
+def test_prompt_in_a_graph(q):
+    """Prompt attention captured once and replayed on new inputs, bit for bit."""
+    import torch
+    g = np.random.default_rng(1310)
+    n = 150
+    x = torch.zeros((n, 8, 64), dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, 60, n], dtype=torch.int32, device="cuda")
+
+    def call(t):
+        qt, kt, vt = t.split((4, 2, 2), 1)
+        return q.prompt_attention(qt, kt, vt, off, off, max_q=90, window=40, sinks=2)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(x)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(x)
+    for rep in range(3):
+        print("graph replay %d" % rep, flush=True)
+        x.copy_(rand16(g, tuple(x.shape), "bf16")[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, call(x.clone())), rep
