@@ -1,0 +1,25 @@
+"""Attention on the GPU at the ends of its arguments' ranges, against float64:
+windows and sinks up to 2^31 - 1, scales, strides that are never used, and sizes
+that reach every dispatched kernel (bounds and formulas: attention_model.py)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from tests import attention_model as model
+from tests.gpu_common import host
+from tests.test_gpu_attention import Cache, check_decode, check_prompt, close, f64, q, rand16, rope_table  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+MOST = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("d", [64, 128, 200])
+@pytest.mark.parametrize("window", [2 ** 30, MOST - 6, MOST])
+@pytest.mark.parametrize("nq,nk", [(10, 5), (300, 70), (5, 10)])
+def test_prompt_window_past_every_key(q, d, window, nq, nk):
+    """A window wider than the cache hides nothing, also where the first queries see no key."""
+    g = np.random.default_rng(2000 + nq + d)
+    check_prompt(q, g, [nq, 4], [nk, 4], 2, 1, d, "bf16", window, 0)
+    check_prompt(q, g, [nq, 4], [nk, 4], 2, 1, d, "bf16", window, 3)
