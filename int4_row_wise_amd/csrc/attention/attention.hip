@@ -140,7 +140,7 @@ int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q
   a.q_heads = q_heads, a.kv_heads = kv_heads, a.dim = dim;
   a.q_offsets = q_offsets, a.k_offsets = k_offsets;
   a.window = window < k_tokens ? window : 0;  // one as long as all keys hides none
-  a.sinks = a.window ? sinks : 0;
+  a.sinks = a.window ? (int)(sinks < k_tokens ? sinks : k_tokens) : 0;  // steps are counted past them in 32 bits
   a.scale = scale;
   a.out = out, a.lse = lse, a.err_count = err_count;
   if (max_q == 0 || max_q > q_tokens) max_q = q_tokens;

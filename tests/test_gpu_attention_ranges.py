@@ -23,3 +23,12 @@ def test_prompt_window_past_every_key(q, d, window, nq, nk):
     g = np.random.default_rng(2000 + nq + d)
     check_prompt(q, g, [nq, 4], [nk, 4], 2, 1, d, "bf16", window, 0)
     check_prompt(q, g, [nq, 4], [nk, 4], 2, 1, d, "bf16", window, 3)
+
+
+@pytest.mark.parametrize("d", [64, 200])
+@pytest.mark.parametrize("window", [1, 40])
+@pytest.mark.parametrize("sinks", [MOST - 33, MOST - 30, MOST])
+def test_prompt_sinks_past_every_key(q, d, window, sinks):
+    """More sinks than keys: a window hides nothing."""
+    g = np.random.default_rng(2100 + d)
+    check_prompt(q, g, [200, 30], [200, 90], 2, 1, d, "bf16", window, sinks)
