@@ -99,6 +99,7 @@ int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, 
  *   out      [q_tokens][q_heads][dim]; lse [q_tokens][q_heads] fp32, nullable
  * Rows that no sequence covers are left as they are.  A sequence whose
  * offsets decrease or leave the arrays is skipped and counted once.
+ * q_tokens (times q_heads / kv_heads) and k_tokens: at most 2^31 - 1024.
  */
 int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q_tokens,
                           int64_t k_tokens, int32_t batch, int32_t q_heads, int32_t kv_heads,

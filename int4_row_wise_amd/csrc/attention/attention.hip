@@ -24,6 +24,7 @@ namespace {
 constexpr int kWave = 64;
 constexpr int kBlock = 256;
 constexpr int64_t kMaxBlocks = (1 << 24) - 1;  // of kBlock threads: a launch counts threads in 32 bits
+constexpr int64_t kMostPlaces = INT32_MAX - 1023;  // rows, keys and slots are counted in 32 bits, up to a step past the last
 
 #include "../common.inc"
 #include "rows.inc"
@@ -120,7 +121,7 @@ int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q
                           int64_t max_q, int32_t window, int32_t sinks, float scale, void* out,
                           float* lse, int32_t* err_count, qemb_stream_t stream) {
   if (q_tokens < 0 || k_tokens < 0 || batch < 0 || window < 0 || sinks < 0 || max_q < 0) return QEMB_E_INVALID_ARG;
-  if (q_tokens > INT32_MAX || k_tokens > INT32_MAX) return QEMB_E_UNSUPPORTED;
+  if (q_tokens > kMostPlaces || k_tokens > kMostPlaces) return QEMB_E_UNSUPPORTED;
   // a tile's byte offsets are 32 bits wide
   if (k_token_stride > kMaxTokenStride || v_token_stride > kMaxTokenStride) return QEMB_E_UNSUPPORTED;
   if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
