@@ -126,6 +126,7 @@ int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q
  * A sequence of length 0 gives zeros and lse = -inf, and so does one whose
  * length leaves its range, which is counted.  The rows of a page outside
  * [0, pages) are taken as not visible and counted (at least once).
+ * width * page_size: at most 2^31 - 1024.
  */
 size_t qemb_decode_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,
                                    int32_t width, int32_t page_size, int32_t window, int32_t sinks,

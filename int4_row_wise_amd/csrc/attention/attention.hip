@@ -153,7 +153,7 @@ size_t qemb_decode_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_he
                                    int32_t width, int32_t page_size, int32_t window, int32_t sinks,
                                    int32_t with_mass) {
   if (batch < 1 || check_groups(q_heads, kv_heads, dim, QEMB_DTYPE_BF16) != QEMB_OK || width < 1 || !is_pow2(page_size) ||
-      window < 0 || sinks < 0 || (int64_t)width * page_size > INT32_MAX)
+      window < 0 || sinks < 0 || (int64_t)width * page_size > kMostPlaces)
     return 0;
   return decode_plan(batch, q_heads, kv_heads, dim, (int64_t)width * page_size, window, sinks, with_mass != 0).bytes;
 }
@@ -167,7 +167,7 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
   if (batch < 0 || width < 0 || pages < 0 || window < 0 || sinks < 0 || !is_pow2(page_size)) return QEMB_E_INVALID_ARG;
   if (bits != 16 && bits != 8 && bits != 4) return QEMB_E_INVALID_ARG;
   if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
-  if ((int64_t)width * page_size > INT32_MAX) return QEMB_E_UNSUPPORTED;
+  if ((int64_t)width * page_size > kMostPlaces) return QEMB_E_UNSUPPORTED;
   if ((int64_t)kv_heads * page_size > INT32_MAX || (int64_t)kv_heads * page_size * row_bytes_of(dim, bits) > INT32_MAX)
     return QEMB_E_UNSUPPORTED;  // a page's bytes are counted in 32 bits
   if (batch == 0) return QEMB_OK;

@@ -16,3 +16,11 @@ MOST = 2 ** 31 - 1
 ])
 def test_prompt_rows_and_keys_near_2_31_are_refused(lib, change):  # noqa: F811
     assert call(lib.qemb_prompt_attention, PROMPT, **change) == -3
+
+
+@pytest.mark.parametrize("page,width", [(1, MOST), (16, 2 ** 27 - 1), (1024, 2 ** 21 - 1)])
+def test_decode_tables_near_2_31_slots_are_refused(lib, page, width):  # noqa: F811
+    assert call(lib.qemb_decode_attention, DECODE, page=page, width=width, mass=None) == -3
+    assert call(lib.qemb_decode_attention, DECODE, page=page, width=width, window=100) == -3
+    assert lib.qemb_decode_workspace_bytes(2, 4, 2, 64, width, page, 0, 0, 1) == 0
+    assert lib.qemb_decode_workspace_bytes(2, 4, 2, 64, (2 ** 31 - 1024) // page, page, 0, 0, 1) > 0
