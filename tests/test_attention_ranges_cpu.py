@@ -18,7 +18,7 @@ def test_prompt_rows_and_keys_near_2_31_are_refused(lib, change):  # noqa: F811
     assert call(lib.qemb_prompt_attention, PROMPT, **change) == -3
 
 
-@pytest.mark.parametrize("page,width", [(1, MOST), (16, 2 ** 27 - 1), (1024, 2 ** 21 - 1)])
+@pytest.mark.parametrize("page,width", [(1, MOST), (16, 2 ** 27 - 1), (512, 2 ** 22 - 1)])
 def test_decode_tables_near_2_31_slots_are_refused(lib, page, width):  # noqa: F811
     assert call(lib.qemb_decode_attention, DECODE, page=page, width=width, mass=None) == -3
     assert call(lib.qemb_decode_attention, DECODE, page=page, width=width, window=100) == -3
