@@ -159,6 +159,7 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
  * A length outside [0, min(width * page_size, mass_len)] is taken as 0 and
  * counted; a row whose old page lies outside its array is copied as zeros, one
  * whose new page does is not copied; both are counted.
+ * min(width * page_size, mass_len): at most 2^31 - 1024.
  */
 int qemb_evict(const void* k_pages, const void* v_pages, int64_t pages, int32_t page_size,
                int64_t row_bytes, int32_t batch, int32_t kv_heads, const int32_t* block_table,

@@ -209,6 +209,7 @@ int qemb_evict(const void* k_pages, const void* v_pages, int64_t pages, int32_t 
   if (row_bytes > (1 << 16) || (int64_t)width * page_size > INT32_MAX || (int64_t)new_width * page_size > INT32_MAX ||
       mass_len > INT32_MAX || new_mass_len > INT32_MAX || (int64_t)batch * kv_heads > INT32_MAX)
     return QEMB_E_UNSUPPORTED;
+  if ((int64_t)width * page_size > kMostPlaces && mass_len > kMostPlaces) return QEMB_E_UNSUPPORTED;  // both bound a length
   if (batch == 0) return QEMB_OK;
   if (!seq_lens || !new_block_table || !kept || !new_mass || !new_lens || (width > 0 && (!block_table)) ||
       (mass_len > 0 && !mass) || (pages > 0 && (!k_pages || !v_pages)) || (new_pages > 0 && (!new_k_pages || !new_v_pages)))

@@ -24,3 +24,11 @@ def test_decode_tables_near_2_31_slots_are_refused(lib, page, width):  # noqa: F
     assert call(lib.qemb_decode_attention, DECODE, page=page, width=width, window=100) == -3
     assert lib.qemb_decode_workspace_bytes(2, 4, 2, 64, width, page, 0, 0, 1) == 0
     assert lib.qemb_decode_workspace_bytes(2, 4, 2, 64, (2 ** 31 - 1024) // page, page, 0, 0, 1) > 0
+
+
+@pytest.mark.parametrize("change", [
+    dict(page=1, width=MOST, mass_len=MOST, new_width=20), dict(page=16, width=2 ** 27 - 1, mass_len=MOST - 15),
+    dict(page=512, width=2 ** 22 - 1, mass_len=MOST - 1022),
+])
+def test_evict_slots_near_2_31_are_refused(lib, change):  # noqa: F811
+    assert call(lib.qemb_evict, EVICT, **change) == -3
