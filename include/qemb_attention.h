@@ -71,7 +71,7 @@ extern "C" {
  *               nothing to the cache
  * A token whose position leaves [0, places) gives zero rows in q_out and
  * k_out and nothing in the cache; a slot past the cache writes nothing there;
- * each is counted once.
+ * each is counted once.  q_heads + 2 kv_heads: at most 2^31 - 1024.
  */
 int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, int32_t q_heads,
                    int32_t kv_heads, int32_t dim, int32_t dtype, int64_t q_token_stride,

@@ -77,6 +77,7 @@ int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, 
   if (int rc = check_heads(q_heads, kv_heads, dim, dtype)) return rc;
   if (rot_dim % 16) return QEMB_E_UNSUPPORTED;
   const bool cached = k_pages || v_pages;
+  if (q_heads + (cached ? 2 : 1) * (int64_t)kv_heads > kMostPlaces) return QEMB_E_UNSUPPORTED;
   if (cached) {
     if (!k_pages || !v_pages || !is_pow2(page_size)) return QEMB_E_INVALID_ARG;
     if (bits != 16 && bits != 8 && bits != 4) return QEMB_E_INVALID_ARG;

@@ -32,3 +32,11 @@ def test_decode_tables_near_2_31_slots_are_refused(lib, page, width):  # noqa: F
 ])
 def test_evict_slots_near_2_31_are_refused(lib, change):  # noqa: F811
     assert call(lib.qemb_evict, EVICT, **change) == -3
+
+
+@pytest.mark.parametrize("change", [
+    dict(hq=2 ** 30, hkv=2 ** 29), dict(hq=MOST), dict(hq=MOST - 1030, hkv=8), dict(hkv=MOST),
+    dict(hq=2 ** 30, hkv=2 ** 30, v=None, k_pages=None, v_pages=None),
+])
+def test_norm_rope_heads_near_2_31_are_refused(lib, change):  # noqa: F811
+    assert call(lib.qemb_norm_rope, NORM, **change) == -3
