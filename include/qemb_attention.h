@@ -27,7 +27,8 @@
  * dim (of one head) is a multiple of 8, 8 .. QEMB_MAX_HEAD_DIM; in the
  * attentions q_heads is a multiple of kv_heads, and query head h reads kv head
  * h / (q_heads / kv_heads).  dtype is that of queries, 16-bit rows, weights
- * and outputs.  Sums, softmax statistics and norms are held in binary32.
+ * and outputs.  Sums, softmax statistics and norms are held in binary32.  The
+ * scale of the scores is finite, of any sign.
  *
  * Conventions (those of qemb.h): every array is a device pointer owned by
  * the caller; nothing is allocated, kept or synchronized; work goes onto

@@ -122,6 +122,7 @@ int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q
                           int64_t max_q, int32_t window, int32_t sinks, float scale, void* out,
                           float* lse, int32_t* err_count, qemb_stream_t stream) {
   if (q_tokens < 0 || k_tokens < 0 || batch < 0 || window < 0 || sinks < 0 || max_q < 0) return QEMB_E_INVALID_ARG;
+  if (!isfinite(scale)) return QEMB_E_INVALID_ARG;
   if (q_tokens > kMostPlaces || k_tokens > kMostPlaces) return QEMB_E_UNSUPPORTED;
   // a tile's byte offsets are 32 bits wide
   if (k_token_stride > kMaxTokenStride || v_token_stride > kMaxTokenStride) return QEMB_E_UNSUPPORTED;
@@ -166,6 +167,7 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
                           float scale, float* mass, int64_t mass_len, void* out, float* lse,
                           void* workspace, int32_t* err_count, qemb_stream_t stream) {
   if (batch < 0 || width < 0 || pages < 0 || window < 0 || sinks < 0 || !is_pow2(page_size)) return QEMB_E_INVALID_ARG;
+  if (!isfinite(scale)) return QEMB_E_INVALID_ARG;
   if (bits != 16 && bits != 8 && bits != 4) return QEMB_E_INVALID_ARG;
   if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
   if ((int64_t)width * page_size > kMostPlaces) return QEMB_E_UNSUPPORTED;

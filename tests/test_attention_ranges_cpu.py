@@ -40,3 +40,9 @@ def test_evict_slots_near_2_31_are_refused(lib, change):  # noqa: F811
 ])
 def test_norm_rope_heads_near_2_31_are_refused(lib, change):  # noqa: F811
     assert call(lib.qemb_norm_rope, NORM, **change) == -3
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_scales_that_are_not_finite_are_refused(lib, scale):  # noqa: F811
+    assert call(lib.qemb_prompt_attention, PROMPT, scale=scale) == -1
+    assert call(lib.qemb_decode_attention, DECODE, scale=scale) == -1
