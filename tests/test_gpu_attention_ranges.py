@@ -32,3 +32,16 @@ def test_prompt_sinks_past_every_key(q, d, window, sinks):
     """More sinks than keys: a window hides nothing."""
     g = np.random.default_rng(2100 + d)
     check_prompt(q, g, [200, 30], [200, 90], 2, 1, d, "bf16", window, sinks)
+
+
+def test_prompt_small_scale(q):
+    """Products of 2^100 and a scale of 2^-103."""
+    import torch
+    g = np.random.default_rng(2200)
+    n, d, scale = 90, 64, 2.0 ** -103
+    (qt, qv), (kt, kv), (vt, vv) = (rand16(g, (n, 1, d), "bf16", s) for s in (2.0 ** 50, 2.0 ** 50, 1.0))
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out = f64(q.prompt_attention(qt, kt, vt, off, off, scale=scale))
+    for i in range(n):
+        o, ob, *_ = model.attend(qv[i, 0], kv[:, 0], vv[:, 0], model.visible(i, n, 0, 0), scale, "bf16")
+        close(out[i, 0], o, ob, "row %d" % i)
