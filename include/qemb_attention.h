@@ -61,8 +61,9 @@ extern "C" {
  * rot_dim on are not rotated.  Values are only copied (or packed).  Packed
  * rows hold the binary32 results encoded by the range rule of qemb.h.
  *   q, k, v     [tokens][heads][dim] of dtype, with strides in elements
- *               between tokens and between heads (multiples of 8), dim
- *               contiguous, 16-byte aligned; v only with pages
+ *               between tokens and between heads (multiples of 8; a stride
+ *               along one token or one head is not read), dim contiguous,
+ *               16-byte aligned; v only with pages
  *   positions   [tokens] of index_type, each in [0, places)
  *   cos_sin     [places][rot_dim] fp32; rot_dim a multiple of 16, <= dim
  *   q_weight, k_weight  [dim] of dtype, or NULL for ones

@@ -55,6 +55,9 @@ inline bool strides_fit(int64_t token, int64_t head) {
   return token >= 0 && head >= 0 && token % 8 == 0 && head % 8 == 0;
 }
 
+// A stride along one token or one head is never taken, so it may be anything.
+inline int64_t taken(int64_t stride, int64_t count, int32_t dim) { return count > 1 ? stride : dim; }
+
 inline int64_t row_bytes_of(int32_t dim, int32_t bits) {
   return bits == 16 ? 2 * (int64_t)dim : ((int64_t)dim * bits / 8 + 4 + 15) / 16 * 16;
 }
@@ -82,6 +85,9 @@ int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, 
     if (!k_pages || !v_pages || !is_pow2(page_size)) return QEMB_E_INVALID_ARG;
     if (bits != 16 && bits != 8 && bits != 4) return QEMB_E_INVALID_ARG;
   }
+  q_token_stride = taken(q_token_stride, tokens, dim), q_head_stride = taken(q_head_stride, q_heads, dim);
+  k_token_stride = taken(k_token_stride, tokens, dim), k_head_stride = taken(k_head_stride, kv_heads, dim);
+  v_token_stride = taken(v_token_stride, tokens, dim), v_head_stride = taken(v_head_stride, kv_heads, dim);
   if (!strides_fit(q_token_stride, q_head_stride) || !strides_fit(k_token_stride, k_head_stride) ||
       (cached && !strides_fit(v_token_stride, v_head_stride)))
     return QEMB_E_MISALIGNED;
@@ -124,9 +130,12 @@ int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q
   if (q_tokens < 0 || k_tokens < 0 || batch < 0 || window < 0 || sinks < 0 || max_q < 0) return QEMB_E_INVALID_ARG;
   if (!isfinite(scale)) return QEMB_E_INVALID_ARG;
   if (q_tokens > kMostPlaces || k_tokens > kMostPlaces) return QEMB_E_UNSUPPORTED;
+  if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
+  q_token_stride = taken(q_token_stride, q_tokens, dim), q_head_stride = taken(q_head_stride, q_heads, dim);
+  k_token_stride = taken(k_token_stride, k_tokens, dim), k_head_stride = taken(k_head_stride, kv_heads, dim);
+  v_token_stride = taken(v_token_stride, k_tokens, dim), v_head_stride = taken(v_head_stride, kv_heads, dim);
   // a tile's byte offsets are 32 bits wide
   if (k_token_stride > kMaxTokenStride || v_token_stride > kMaxTokenStride) return QEMB_E_UNSUPPORTED;
-  if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
   if (!strides_fit(q_token_stride, q_head_stride) || !strides_fit(k_token_stride, k_head_stride) ||
       !strides_fit(v_token_stride, v_head_stride))
     return QEMB_E_MISALIGNED;

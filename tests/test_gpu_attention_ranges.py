@@ -45,3 +45,31 @@ def test_prompt_small_scale(q):
     for i in range(n):
         o, ob, *_ = model.attend(qv[i, 0], kv[:, 0], vv[:, 0], model.visible(i, n, 0, 0), scale, "bf16")
         close(out[i, 0], o, ob, "row %d" % i)
+
+
+def odd(t, dim, stride):
+    """t with an odd stride along a dimension of size 1."""
+    strides = list(t.stride())
+    assert t.shape[dim] == 1
+    strides[dim] = stride
+    return t.as_strided(t.shape, strides)
+
+
+def test_stride_of_one_token_or_head_is_not_used(q):
+    import torch
+    g = np.random.default_rng(2300)
+    qt, _ = rand16(g, (1, 3, 64), "bf16")
+    kt, _ = rand16(g, (1, 1, 64), "bf16")
+    vt, _ = rand16(g, (1, 1, 64), "bf16")
+    off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    pos, cs = torch.tensor([7], dtype=torch.int32, device="cuda"), torch.from_numpy(rope_table(10, 64)).cuda()
+    pages = [torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    slot = torch.zeros(1, dtype=torch.int64, device="cuda")
+    want = q.prompt_attention(qt, kt, vt, off, off)
+    want_q, _ = q.norm_rope(qt, kt, pos, cs, v=vt, k_pages=pages[0], v_pages=pages[1], slots=slot)
+    for stride in (5, 1 << 40):
+        qs, ks, vs = odd(qt, 0, stride), odd(odd(kt, 0, stride), 1, 3), odd(odd(vt, 0, 1), 1, stride)
+        assert torch.equal(q.prompt_attention(qs, ks, vs, off, off), want)
+        got_q, _ = q.norm_rope(qs, ks, pos, cs, v=vs, k_pages=pages[2], v_pages=pages[3], slots=slot)
+        assert torch.equal(got_q, want_q)
+        assert torch.equal(pages[2], pages[0]) and torch.equal(pages[3], pages[1])
