@@ -88,6 +88,12 @@ def _device(name: str, t: torch.Tensor) -> int:
     return t.get_device()
 
 
+def _int32(name: str, value: int) -> None:
+    """Refuses a number that the C ABI's 32 bits would cut."""
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError("%s must fit 32 bits, got %d" % (name, value))
+
+
 def _want(name: str, t: torch.Tensor, shape: tuple, dtype, dev: int) -> None:
     """A contiguous tensor of a given shape and type on a given GPU."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
@@ -213,6 +219,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offset
     n, hq, d = q.shape
     if k.shape != v.shape or k.shape[2] != d:
         raise ValueError("k and v must be [tokens, kv_heads, %d] alike" % d)
+    _int32("window", window)
+    _int32("sinks", sinks)
     if not isinstance(q_offsets, torch.Tensor) or q_offsets.numel() < 1:
         raise ValueError("q_offsets must have batch + 1 entries")
     batch = q_offsets.numel() - 1
@@ -236,6 +244,9 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offset
 def decode_workspace_bytes(batch: int, q_heads: int, kv_heads: int, dim: int, width: int, page_size: int,
                            window: int = 0, sinks: int = 0, with_mass: bool = False) -> int:
     """Bytes of workspace that decode_attention needs for these sizes."""
+    for name, value in (("batch", batch), ("q_heads", q_heads), ("kv_heads", kv_heads), ("dim", dim), ("width", width),
+                        ("page_size", page_size), ("window", window), ("sinks", sinks)):
+        _int32(name, value)
     return int(load_attention_library().qemb_decode_workspace_bytes(
         batch, q_heads, kv_heads, dim, width, page_size, window, sinks, int(with_mass)))
 
@@ -255,6 +266,8 @@ def decode_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     dev, dtype = _device("q", q), q.dtype
     if q.dim() != 3 or dtype not in _DTYPES or not q.is_contiguous():
         raise TypeError("q must be [batch, heads, dim] of bfloat16 or float16, contiguous")
+    _int32("window", window)
+    _int32("sinks", sinks)
     b, hq, d = q.shape
     pages, hkv, size = _cache(k_pages, v_pages, d, bits, dtype, dev)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
@@ -322,6 +335,7 @@ def evict(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tenso
     _want("block_table", block_table, (b, width), torch.int32, dev)
     _want("new_block_table", new_block_table, (b, new_width), torch.int32, dev)
     _want("mass", mass, (b, hkv, mass_len), torch.float32, dev)
+    _int32("keep", keep)
     if keep < 1 or sinks < 0 or recent < 0 or sinks + recent > keep or new_width * size < keep:
         raise ValueError("keep must be at least 1 and sinks + recent, and fit the new pages")
     if kept is None:

@@ -73,3 +73,24 @@ def test_stride_of_one_token_or_head_is_not_used(q):
         got_q, _ = q.norm_rope(qs, ks, pos, cs, v=vs, k_pages=pages[2], v_pages=pages[3], slots=slot)
         assert torch.equal(got_q, want_q)
         assert torch.equal(pages[2], pages[0]) and torch.equal(pages[3], pages[1])
+
+
+def test_numbers_past_32_bits_are_refused(q):
+    """An argument that a 32-bit integer does not hold is refused, not cut."""
+    import torch
+    x = torch.zeros((4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    pages = torch.zeros((3, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((4, 1), dtype=torch.int32, device="cuda")
+    lens = torch.ones(4, dtype=torch.int32, device="cuda")
+    mass = torch.zeros((4, 2, 16), device="cuda")
+    for n in (2 ** 31, 2 ** 32 + 2, 2 ** 63 - 1, -2 ** 32):
+        for name in ("window", "sinks"):
+            with pytest.raises(ValueError):
+                q.prompt_attention(x, x, x, off, off, **{name: n})
+            with pytest.raises(ValueError):
+                q.decode_attention(x, pages, pages, table, lens, **{name: n})
+            with pytest.raises(ValueError):
+                q.decode_workspace_bytes(4, 2, 2, 64, 1, 16, **{name: n})
+        with pytest.raises(ValueError):
+            q.evict(pages, pages, table, lens, mass, n, pages, pages, table)
