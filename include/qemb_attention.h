@@ -27,7 +27,11 @@
  * dim (of one head) is a multiple of 8, 8 .. QEMB_MAX_HEAD_DIM; in the
  * attentions q_heads is a multiple of kv_heads, and query head h reads kv head
  * h / (q_heads / kv_heads).  dtype is that of queries, 16-bit rows, weights
- * and outputs.  Sums, softmax statistics and norms are held in binary32.  The
+ * and outputs.  Sums, softmax statistics and norms are held in binary32; for
+ * the second product of the attentions each key's weight is rounded to the
+ * 16-bit type, and over packed rows weight times scale to binary16 (and the
+ * query, scaled to a largest element of 1 to 2, too: to at most 2^-25), so that
+ * an output is off by up to that rounding of its weights and its own.  The
  * scale of the scores is finite, of any sign.
  *
  * Conventions (those of qemb.h): every array is a device pointer owned by
@@ -35,7 +39,9 @@
  * `stream`; errors that the host can see return before anything is enqueued.
  * Bad device data never faults: it is skipped as stated and, where an
  * err_count (nullable, device, caller-zeroed) is taken, counted.  Calls are
- * deterministic: equal inputs give equal bits.
+ * deterministic: equal calls give equal bits.  (Another batch size or width of
+ * the block table moves the borders at which qemb_decode_attention splits its
+ * sums, and with them the last bits.)
  */
 #ifndef QEMB_ATTENTION_H
 #define QEMB_ATTENTION_H
@@ -96,11 +102,15 @@ int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, 
  *            as in qemb_norm_rope
  *   q_offsets, k_offsets  [batch + 1] int32
  *   max_q    the longest query run expected (a hint for the grid: longer runs
- *            are still computed)
+ *            are still computed); 0 = q_tokens, for every sequence, which
+ *            launches batch times as many workgroups as have work
  *   window   0 = unlimited; sinks >= 0, read only with a window
  *   out      [q_tokens][q_heads][dim]; lse [q_tokens][q_heads] fp32, nullable
  * Rows that no sequence covers are left as they are.  A sequence whose
  * offsets decrease or leave the arrays is skipped and counted once.
+ * A row whose statistics are finite but whose result is not (an infinity or a
+ * NaN among the values it sees, or in a tile beside them) is computed again,
+ * one key after another: right, but at a small part of the speed.
  * q_tokens (times q_heads / kv_heads) and k_tokens: at most 2^31 - 1024.
  */
 int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q_tokens,
@@ -117,7 +127,10 @@ int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q
  * qemb_prompt_attention.
  *   q            [batch][q_heads][dim], contiguous
  *   k_pages, v_pages  the cache of `pages` pages
- *   block_table  [batch][width] int32
+ *   block_table  [batch][width] int32; width * page_size (or the window, where
+ *                it is less) and batch set the split of the work and the
+ *                workspace, whatever the lengths are: a table much wider than
+ *                the longest sequence costs both
  *   seq_lens     [batch] int32, each in [0, width * page_size]
  *   mass         [batch][kv_heads][mass_len] fp32 or NULL: mass[b][h][j] grows
  *                by the sum over kv head h's query heads of key j's weight

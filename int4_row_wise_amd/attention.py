@@ -211,7 +211,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offset
     (any strides between tokens and heads), sequence b in rows
     [offsets[b], offsets[b + 1]); its last query stands at its last key.  With a
     window, a query sees the last `window` keys up to its own and the first
-    `sinks` keys.  max_q (the longest run of queries) only shapes the grid.
+    `sinks` keys.  max_q (the longest run of queries) only shapes the grid; left
+    at 0, every sequence gets workgroups for all queries.
     scale: 1 / sqrt(d) unless given.  Returns out [Nq, Hq, d]; lse [Nq, Hq]
     float32 is filled if given."""
     dev, dtype = _device("q", q), q.dtype
@@ -261,7 +262,9 @@ def decode_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     seq_lens[b] rows of its pages block_table[b] (int32; the token's own row is
     the last).  window and sinks as in prompt_attention.  mass [B, Hkv, M]
     float32 (M >= every length) grows by each key's softmax weight, summed over
-    the query heads of its kv head.  Returns out [B, Hq, d]; lse [B, Hq] float32
+    the query heads of its kv head.  The table's width (not the lengths) sets how
+    the work is split and the workspace, so it is best kept near the longest
+    sequence.  Returns out [B, Hq, d]; lse [B, Hq] float32
     is filled if given."""
     dev, dtype = _device("q", q), q.dtype
     if q.dim() != 3 or dtype not in _DTYPES or not q.is_contiguous():
