@@ -61,8 +61,8 @@ def draw(rng):
         return dict(op=op, batch=batch, groups=rng.choice((1, 1, 2, 5)), prefix=_log_int(rng, 1, min(32768, 4194304 // (batch * group))), own_len=_log_int(rng, 1, min(2048, 65536 // batch)),
                     hq=hkv * group, hkv=hkv, d=rng.choice((64, 96, 128)), dtype=dtype, bits=rng.choice((16, 16, 8, 4)), page=rng.choice((8, 16, 32, 64, 128)))
     if op == "add_norm":
-        dim = 8 * _log_int(rng, 8, 1024)
         form = rng.choice(("values", "values", "int8", "fp8", "rows8"))
+        dim = 8 * _log_int(rng, 8, 128 if form == "rows8" else 1024)  # packed rows end at 1024 elements
         return dict(op=op, tokens=_log_int(rng, 1, min(16384, (1 << 27) // dim)), dim=dim, dtype=dtype, form=form, group=rng.choice((0, 32, 128)) if form in ("int8", "fp8") and dim % 128 == 0 else 0)
     vocab = _log_int(rng, 500, 200000)
     dtype = rng.choice(("bf16", "fp16", "fp32"))
