@@ -12,6 +12,9 @@
  *  - qemb_decode_attention  attention of one new token over the cache, split
  *                         over the cache's length and joined; optionally adds
  *                         every key's weight to a running mass
+ *  - qemb_shared_attention  attention of one new token for each sequence of a
+ *                         batch whose sequences share prefixes, read once a
+ *                         group of sequences
  *  - qemb_evict           keeps a budget of rows by accumulated mass and
  *                         copies them to other pages
  *
@@ -56,6 +59,7 @@ extern "C" {
 #define QEMB_DTYPE_FP16 1
 
 #define QEMB_MAX_HEAD_DIM 256
+#define QEMB_MAX_AXES 4
 
 /*
  * Norm, rotation and append.  For every token t and head, in binary32:
@@ -90,6 +94,27 @@ int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, 
                    void* q_out, void* k_out, void* k_pages, void* v_pages, const int64_t* slots,
                    int64_t pages, int32_t page_size, int32_t bits, int32_t* err_count,
                    qemb_stream_t stream);
+
+/*
+ * The same with positions on several axes (time, height and width of an
+ * image's or a video's patches), and with the norm left out where norm = 0
+ * (weights NULL then; eps is not read):
+ *   positions   [axes][tokens] of index_type, axes 1 .. QEMB_MAX_AXES, each in
+ *               [0, places); a token with one that is not is skipped as above
+ *   pair_axes   [rot_dim/2], 4-byte aligned: pair i turns by the position on axis
+ *               pair_axes[i], cos = cos_sin[positions[pair_axes[i]][t]][i]; a pair
+ *               whose number is no axis is not turned.  NULL (axis 0 for all) with
+ *               axes = 1 only
+ */
+int qemb_norm_rope_axes(const void* q, const void* k, const void* v, int64_t tokens, int32_t q_heads,
+                        int32_t kv_heads, int32_t dim, int32_t dtype, int64_t q_token_stride,
+                        int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                        int64_t v_token_stride, int64_t v_head_stride, const void* positions,
+                        int32_t axes, const uint8_t* pair_axes, int32_t index_type, const float* cos_sin,
+                        int64_t places, int32_t rot_dim, int32_t interleaved, int32_t norm,
+                        const void* q_weight, const void* k_weight, float eps, void* q_out, void* k_out,
+                        void* k_pages, void* v_pages, const int64_t* slots, int64_t pages,
+                        int32_t page_size, int32_t bits, int32_t* err_count, qemb_stream_t stream);
 
 /*
  * Attention of prompts.  Sequence b has queries [q_offsets[b],
@@ -153,6 +178,43 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
                           int32_t width, const int32_t* seq_lens, int32_t window, int32_t sinks,
                           float scale, float* mass, int64_t mass_len, void* out, float* lse,
                           void* workspace, int32_t* err_count, qemb_stream_t stream);
+
+/*
+ * Attention of one new token for each sequence of a batch whose sequences
+ * share prefixes: group g holds the sequences [group_offsets[g],
+ * group_offsets[g+1]), and each of their tokens sees the prefix_lens[g] rows of
+ * the pages prefix_table[g] and then its sequence's own seq_lens[b] rows of the
+ * pages block_table[b] (its own row among them):
+ *     out = sum_j softmax_j(scale q.k_j) v_j,  lse = log sum_j exp(scale q.k_j)
+ * Equal rows give the bits of the same sums in another order than
+ * qemb_decode_attention's.
+ *   q, k_pages, v_pages, block_table [batch][width], seq_lens  as in
+ *                qemb_decode_attention; a length may be 0 here
+ *   prefix_table [groups][prefix_width] int32, prefix_lens [groups] int32, each
+ *                in [0, prefix_width * page_size]; the two widths, groups and batch
+ *                set the split of the work and the workspace, whatever the lengths are
+ *   group_offsets  [groups + 1] int32, or NULL for one group of all sequences
+ *   out          [batch][q_heads][dim]; lse [batch][q_heads] fp32, nullable
+ *   workspace    qemb_shared_workspace_bytes(...) bytes, 16-byte aligned;
+ *                contents need not be kept
+ * A sequence that no group holds sees its own rows alone; one that sees nothing
+ * gives zeros and lse = -inf.  A length that leaves its range is taken as 0 and
+ * counted.  Offsets that decrease anywhere or leave [0, batch] make no groups
+ * (every sequence as if no group held it) and are counted once.  The rows of a
+ * page outside [0, pages) are taken as not
+ * visible and counted (at least once).
+ * width * page_size and prefix_width * page_size: at most 2^31 - 1024.
+ */
+size_t qemb_shared_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t groups,
+                                   int32_t prefix_width, int32_t width, int32_t page_size);
+
+int qemb_shared_attention(const void* q, const void* k_pages, const void* v_pages, int64_t pages,
+                          int32_t page_size, int32_t bits, int32_t batch, int32_t q_heads,
+                          int32_t kv_heads, int32_t dim, int32_t dtype, const int32_t* prefix_table,
+                          int32_t prefix_width, const int32_t* prefix_lens, const int32_t* group_offsets,
+                          int32_t groups, const int32_t* block_table, int32_t width,
+                          const int32_t* seq_lens, float scale, void* out, float* lse, void* workspace,
+                          int32_t* err_count, qemb_stream_t stream);
 
 /*
  * Eviction.  For every sequence and kv head of length n: all n slots if

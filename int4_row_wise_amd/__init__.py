@@ -7,7 +7,9 @@ library loads on first use and raises if it was not built; there is no CPU
 fallback.  :mod:`int4_row_wise_amd.synth` draws the seeded synthetic inputs.
 :mod:`int4_row_wise_amd.attention` binds ``libqemb_attention.so``
 (``include/qemb_attention.h``): attention over a paged key-value cache of
-16-bit or packed INT8 / INT4 rows.
+16-bit or packed INT8 / INT4 rows; :mod:`int4_row_wise_amd.serving` binds
+``libqemb_serving.so`` (``include/qemb_serving.h``): the residual's addition
+with a norm and the log probabilities of tokens.
 """
 from .qemb import (  # noqa: F401
     RANGE, GREEDY, SUM, WEIGHTED_SUM, CODEBOOK_ITERS, SYMMETRIC, PERCENTILE, ACIQ, QembError,
@@ -20,4 +22,6 @@ from .qemb import (  # noqa: F401
 )
 from .attention import (  # noqa: F401
     decode_attention, decode_workspace_bytes, evict, load_attention_library, norm_rope, prompt_attention,
+    rotary_axes, shared_attention, shared_workspace_bytes,
 )
+from .serving import add_norm, load_serving_library, logprobs_workspace_bytes, token_logprobs  # noqa: F401

@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -25,10 +25,11 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqemb_attention.so")
 
 MAX_HEAD_DIM = 256
+MAX_AXES = 4
 
 EXPORTED = (
-    "qemb_norm_rope", "qemb_prompt_attention", "qemb_decode_workspace_bytes",
-    "qemb_decode_attention", "qemb_evict",
+    "qemb_norm_rope", "qemb_norm_rope_axes", "qemb_prompt_attention", "qemb_decode_workspace_bytes",
+    "qemb_decode_attention", "qemb_shared_workspace_bytes", "qemb_shared_attention", "qemb_evict",
 )
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
@@ -55,6 +56,9 @@ def load_attention_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.qemb_norm_rope.argtypes = [p, p, p, i64, i32, i32, i32, i32, i64, i64, i64, i64, i64, i64, p, i32, p, i64,
                                  i32, i32, p, p, f32, p, p, p, p, p, i64, i32, i32, p, p]
     L.qemb_norm_rope.restype = ctypes.c_int
+    L.qemb_norm_rope_axes.argtypes = [p, p, p, i64, i32, i32, i32, i32, i64, i64, i64, i64, i64, i64, p, i32, p, i32, p,
+                                      i64, i32, i32, i32, p, p, f32, p, p, p, p, p, i64, i32, i32, p, p]
+    L.qemb_norm_rope_axes.restype = ctypes.c_int
     L.qemb_prompt_attention.argtypes = [p, p, p, i64, i64, i32, i32, i32, i32, i32, i64, i64, i64, i64, i64, i64,
                                         p, p, i64, i32, i32, f32, p, p, p, p]
     L.qemb_prompt_attention.restype = ctypes.c_int
@@ -63,6 +67,11 @@ def load_attention_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.qemb_decode_attention.argtypes = [p, p, p, i64, i32, i32, i32, i32, i32, i32, i32, p, i32, p, i32, i32, f32,
                                         p, i64, p, p, p, p, p]
     L.qemb_decode_attention.restype = ctypes.c_int
+    L.qemb_shared_workspace_bytes.argtypes = [i32] * 8
+    L.qemb_shared_workspace_bytes.restype = ctypes.c_size_t
+    L.qemb_shared_attention.argtypes = [p, p, p, i64, i32, i32, i32, i32, i32, i32, i32, p, i32, p, p, i32, p, i32, p,
+                                        f32, p, p, p, p, p]
+    L.qemb_shared_attention.restype = ctypes.c_int
     L.qemb_evict.argtypes = [p, p, i64, i32, i64, i32, i32, p, i32, p, p, i64, i32, i32, i32, p, p, i64, p, i32,
                              p, p, i64, p, p, p]
     L.qemb_evict.restype = ctypes.c_int
@@ -148,14 +157,19 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin
               eps: float = 1e-6, interleaved: bool = False, v: Optional[torch.Tensor] = None,
               k_pages: Optional[torch.Tensor] = None, v_pages: Optional[torch.Tensor] = None,
               slots: Optional[torch.Tensor] = None, bits: int = 16, q_out: Optional[torch.Tensor] = None,
-              k_out: Optional[torch.Tensor] = None,
-              err_count: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+              k_out: Optional[torch.Tensor] = None, err_count: Optional[torch.Tensor] = None,
+              pair_axes: Optional[torch.Tensor] = None, norm: bool = True) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Norm of each head of q [N, Hq, d] and k [N, Hkv, d] (any strides between
     tokens and heads), then rotation by cos_sin[positions] ([places, R] float32:
     R/2 cosines, R/2 sines).  With k_pages and v_pages, k's result and v are
     written to the flat `slots` [N] int64 (page * page_size + offset; negative:
     not written).  Returns (q_out, k_out); k_out is None with pages unless it is
-    given."""
+    given.
+
+    With pair_axes [R/2] uint8 (see rotary_axes), positions is [axes, N] (at most
+    4 axes) and pair i turns by the position on axis pair_axes[i]; a pair whose
+    number is no axis is not turned.  norm=False leaves the norm out (and takes no
+    weights)."""
     dev, dtype = _device("q", q), q.dtype
     qs, ks, vs = _heads("q", q, dtype, dev), _heads("k", k, dtype, dev), (0, 0)
     n, hq, d = q.shape
@@ -163,11 +177,22 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin
     if k.shape[0] != n or k.shape[2] != d:
         raise ValueError("q and k must have the same tokens and head dim")
     wide = isinstance(positions, torch.Tensor) and positions.dtype is torch.int64
-    _want("positions", positions, (n,), torch.int64 if wide else torch.int32, dev)
+    axes = 1
+    if pair_axes is None:
+        _want("positions", positions, (n,), torch.int64 if wide else torch.int32, dev)
+    else:
+        if not isinstance(positions, torch.Tensor) or positions.dim() != 2 or not 1 <= positions.shape[0] <= MAX_AXES:
+            raise ValueError("positions must be [axes, %d] with at most %d axes" % (n, MAX_AXES))
+        axes = positions.shape[0]
+        _want("positions", positions, (axes, n), torch.int64 if wide else torch.int32, dev)
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights belong to the norm")
     if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [places, rot_dim]")
     places, rot = cos_sin.shape
     _want("cos_sin", cos_sin, (places, rot), torch.float32, dev)
+    if pair_axes is not None:
+        _want("pair_axes", pair_axes, (rot // 2,), torch.uint8, dev)
     if q_weight is not None:
         _want("q_weight", q_weight, (d,), dtype, dev)
     if k_weight is not None:
@@ -195,12 +220,31 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin
         _want("k_out", k_out, (n, hkv, d), dtype, dev)
     if err_count is not None:
         _want("err_count", err_count, (1,), torch.int32, dev)
-    _check("qemb_norm_rope", load_attention_library().qemb_norm_rope(
-        q.data_ptr(), k.data_ptr(), _ptr(v), n, hq, hkv, d, _DTYPES[dtype], qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
-        positions.data_ptr(), INDEX_INT64 if wide else INDEX_INT32, cos_sin.data_ptr(), places, rot, int(interleaved),
-        _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(slots),
-        pages, size, bits, _ptr(err_count), _raw_stream(dev)))
+    index = INDEX_INT64 if wide else INDEX_INT32
+    if pair_axes is None and norm:
+        _check("qemb_norm_rope", load_attention_library().qemb_norm_rope(
+            q.data_ptr(), k.data_ptr(), _ptr(v), n, hq, hkv, d, _DTYPES[dtype], qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+            positions.data_ptr(), index, cos_sin.data_ptr(), places, rot, int(interleaved),
+            _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(slots),
+            pages, size, bits, _ptr(err_count), _raw_stream(dev)))
+    else:
+        _check("qemb_norm_rope_axes", load_attention_library().qemb_norm_rope_axes(
+            q.data_ptr(), k.data_ptr(), _ptr(v), n, hq, hkv, d, _DTYPES[dtype], qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+            positions.data_ptr(), axes, _ptr(pair_axes), index, cos_sin.data_ptr(), places, rot, int(interleaved), int(norm),
+            _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(slots),
+            pages, size, bits, _ptr(err_count), _raw_stream(dev)))
     return q_out, k_out
+
+
+def rotary_axes(sections: Sequence[int], *, in_turn: bool = False, device="cuda") -> torch.Tensor:
+    """The axis of each pair, for norm_rope's pair_axes: sections[a] pairs turn by
+    axis a, one axis after the other, or (in_turn) in turn as long as an axis has
+    pairs left: sections (3, 2, 2) give 0 0 0 1 1 2 2, or 0 1 2 0 1 2 0."""
+    if not 1 <= len(sections) <= MAX_AXES or any(n < 0 for n in sections):
+        raise ValueError("sections must be the pairs of 1 .. %d axes" % MAX_AXES)
+    pairs = [(i, a) if in_turn else (a, i) for a, n in enumerate(sections) for i in range(n)]
+    pairs.sort()
+    return torch.tensor([p[1] if in_turn else p[0] for p in pairs], dtype=torch.uint8, device=device)
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
@@ -302,6 +346,73 @@ def decode_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages, size, bits, b, hq, hkv, d, _DTYPES[dtype],
         block_table.data_ptr(), width, seq_lens.data_ptr(), window, sinks, d ** -0.5 if scale is None else scale,
         _ptr(mass), mass_len, out.data_ptr(), _ptr(lse), _ptr(workspace), _ptr(err_count), _raw_stream(dev)))
+    return out
+
+
+def shared_workspace_bytes(batch: int, q_heads: int, kv_heads: int, dim: int, groups: int, prefix_width: int, width: int,
+                           page_size: int) -> int:
+    """Bytes of workspace that shared_attention needs for these sizes."""
+    for name, value in (("batch", batch), ("q_heads", q_heads), ("kv_heads", kv_heads), ("dim", dim), ("groups", groups),
+                        ("prefix_width", prefix_width), ("width", width), ("page_size", page_size)):
+        _int32(name, value)
+    return int(load_attention_library().qemb_shared_workspace_bytes(
+        batch, q_heads, kv_heads, dim, groups, prefix_width, width, page_size))
+
+
+def shared_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, prefix_table: torch.Tensor,
+                     prefix_lens: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, *,
+                     group_offsets: Optional[torch.Tensor] = None, bits: int = 16, scale: Optional[float] = None,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
+                     err_count: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of one new token for each sequence, q [B, Hq, d], where groups of
+    sequences share a prefix: sequences group_offsets[g] .. group_offsets[g + 1] - 1
+    (int32 [G + 1]; None: one group of all) see the prefix_lens[g] rows of the pages
+    prefix_table[g] (int32 [G, P]), read once for the group, and then the seq_lens[b]
+    rows of their own pages block_table[b] (int32 [B, W]; the token's own row is the
+    last; 0 rows are fine).  The tables' widths (not the lengths) set how the work is
+    split and the workspace, so they are best kept near the longest.  Returns out
+    [B, Hq, d]; lse [B, Hq] float32 is filled if given."""
+    dev, dtype = _device("q", q), q.dtype
+    if q.dim() != 3 or dtype not in _DTYPES or not q.is_contiguous():
+        raise TypeError("q must be [batch, heads, dim] of bfloat16 or float16, contiguous")
+    b, hq, d = q.shape
+    pages, hkv, size = _cache(k_pages, v_pages, d, bits, dtype, dev)
+    if not isinstance(prefix_table, torch.Tensor) or prefix_table.dim() != 2 or prefix_table.shape[0] < 1:
+        raise ValueError("prefix_table must be [groups, width]")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [%d, width]" % b)
+    groups, prefix_width = prefix_table.shape
+    width = block_table.shape[1]
+    _want("prefix_table", prefix_table, (groups, prefix_width), torch.int32, dev)
+    _want("prefix_lens", prefix_lens, (groups,), torch.int32, dev)
+    _want("block_table", block_table, (b, width), torch.int32, dev)
+    _want("seq_lens", seq_lens, (b,), torch.int32, dev)
+    if group_offsets is not None:
+        _want("group_offsets", group_offsets, (groups + 1,), torch.int32, dev)
+    elif groups != 1:
+        raise ValueError("%d prefixes need group_offsets" % groups)
+    if out is None:
+        out = torch.empty((b, hq, d), dtype=dtype, device=q.device)
+    else:
+        _want("out", out, (b, hq, d), dtype, dev)
+    if lse is not None:
+        _want("lse", lse, (b, hq), torch.float32, dev)
+    if err_count is not None:
+        _want("err_count", err_count, (1,), torch.int32, dev)
+    L = load_attention_library()
+    need = L.qemb_shared_workspace_bytes(b, hq, hkv, d, groups, prefix_width, width, size)
+    if workspace is not None:
+        if workspace.numel() < need:
+            raise ValueError("workspace must have at least %d bytes" % need)
+        _want("workspace", workspace, workspace.shape, torch.uint8, dev)
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check("qemb_shared_attention", L.qemb_shared_attention(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages, size, bits, b, hq, hkv, d, _DTYPES[dtype],
+        prefix_table.data_ptr(), prefix_width, prefix_lens.data_ptr(), _ptr(group_offsets), groups,
+        block_table.data_ptr(), width, seq_lens.data_ptr(), d ** -0.5 if scale is None else scale, out.data_ptr(),
+        _ptr(lse), _ptr(workspace), _ptr(err_count), _raw_stream(dev)))
     return out
 
 

@@ -1,5 +1,5 @@
-"""Build libqemb.so and libqemb_attention.so (the HIP C-ABI libraries) in-tree
-for gfx950.
+"""Build libqemb.so, libqemb_attention.so and libqemb_serving.so (the HIP C-ABI
+libraries) in-tree for gfx950.
 
     python -m int4_row_wise_amd.build
 
@@ -28,6 +28,11 @@ ATTN_DIR = os.path.join(CSRC, "attention")
 ATTN_SRC = os.path.join(ATTN_DIR, "attention.hip")
 ATTN_HEADER = os.path.join(ROOT, "include", "qemb_attention.h")
 ATTN_LIB = os.path.join(HERE, "libqemb_attention.so")
+# what stands around the attention in a serving loop: another one
+SERVING_DIR = os.path.join(CSRC, "serving")
+SERVING_SRC = os.path.join(SERVING_DIR, "serving.hip")
+SERVING_HEADER = os.path.join(ROOT, "include", "qemb_serving.h")
+SERVING_LIB = os.path.join(HERE, "libqemb_serving.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
@@ -78,17 +83,27 @@ def build_attention(verbose: bool = False) -> str:
     return ATTN_LIB
 
 
+def build_serving(verbose: bool = False) -> str:
+    """Compile csrc/serving/serving.hip into libqemb_serving.so."""
+    sha = serving_source_sha256()
+    _finish(_compile(SERVING_SRC, SERVING_LIB), verbose)
+    _record(SERVING_LIB, sha)
+    return SERVING_LIB
+
+
 def build(force: bool = True, verbose: bool = False) -> str:
     """Compile csrc/qemb.hip into int4_row_wise_amd/libqemb.so, and beside it
-    the gather floor and the attention library."""
-    if not force and _newer(LIB, source_files() + [HEADER]) and _newer(ATTN_LIB, attention_source_files()):
+    the gather floor, the attention library and the serving library."""
+    if (not force and _newer(LIB, source_files() + [HEADER]) and _newer(ATTN_LIB, attention_source_files())
+            and _newer(SERVING_LIB, serving_source_files())):
         return LIB
     # the hash of the sources as compiled: taken before the compiler reads
     # them, so an edit made while it runs cannot be recorded for this build
     src_hash = source_sha256()
     attn_hash = attention_source_sha256()
+    serving_hash = serving_source_sha256()
     # the small libraries compile beside the large one
-    jobs = [_compile(FLOOR_SRC, FLOOR_LIB), _compile(ATTN_SRC, ATTN_LIB), _compile(SRC, LIB)]
+    jobs = [_compile(FLOOR_SRC, FLOOR_LIB), _compile(ATTN_SRC, ATTN_LIB), _compile(SERVING_SRC, SERVING_LIB), _compile(SRC, LIB)]
     try:
         for job in jobs:
             _finish(job, verbose)
@@ -98,6 +113,7 @@ def build(force: bool = True, verbose: bool = False) -> str:
                 proc.kill()
     _record(LIB, src_hash)
     _record(ATTN_LIB, attn_hash)
+    _record(SERVING_LIB, serving_hash)
     return LIB
 
 
@@ -122,6 +138,17 @@ def attention_source_files() -> list:
 def attention_source_sha256() -> str:
     """sha256 over the attention library's sources, as source_sha256."""
     return _sha256(attention_source_files())
+
+
+def serving_source_files() -> list:
+    """The serving library's sources: its own, the shared helpers and the headers."""
+    own = [os.path.join(SERVING_DIR, f) for f in os.listdir(SERVING_DIR) if f.endswith((".hip", ".inc"))]
+    return sorted(own) + [os.path.join(ATTN_DIR, "rows.inc"), os.path.join(CSRC, "common.inc"), SERVING_HEADER, ATTN_HEADER, HEADER]
+
+
+def serving_source_sha256() -> str:
+    """sha256 over the serving library's sources, as source_sha256."""
+    return _sha256(serving_source_files())
 
 
 def _sha256(paths: list) -> str:
@@ -154,6 +181,8 @@ def ensure_built() -> str:
         return build(force=True)
     if not os.path.exists(ATTN_LIB):
         build_attention()
+    if not os.path.exists(SERVING_LIB):
+        build_serving()
     return LIB
 
 

@@ -4,6 +4,7 @@
 //   * norm_rope_kernel   norms of queries and keys, rotation, append (norm_rope.inc)
 //   * prompt_*           causal / windowed attention of prompts (prompt.inc)
 //   * decode_*           attention of one new token over the pages (decode.inc)
+//   * shared_*           attention of new tokens whose sequences share prefixes (shared.inc)
 //   * evict_*            selection by accumulated mass and the copy (evict.inc)
 // rows.inc holds the row formats: 16-bit rows and the library's packed rows.
 //
@@ -31,6 +32,7 @@ constexpr int64_t kMostPlaces = INT32_MAX - 1023;  // rows, keys and slots are c
 #include "norm_rope.inc"
 #include "prompt.inc"
 #include "decode.inc"
+#include "shared.inc"
 #include "evict.inc"
 
 inline bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -66,16 +68,17 @@ inline int64_t row_bytes_of(int32_t dim, int32_t bits) {
 
 extern "C" {
 
-int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, int32_t q_heads,
-                   int32_t kv_heads, int32_t dim, int32_t dtype, int64_t q_token_stride,
-                   int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
-                   int64_t v_token_stride, int64_t v_head_stride, const void* positions,
-                   int32_t index_type, const float* cos_sin, int64_t places, int32_t rot_dim,
-                   int32_t interleaved, const void* q_weight, const void* k_weight, float eps,
-                   void* q_out, void* k_out, void* k_pages, void* v_pages, const int64_t* slots,
-                   int64_t pages, int32_t page_size, int32_t bits, int32_t* err_count,
-                   qemb_stream_t stream) {
+int qemb_norm_rope_axes(const void* q, const void* k, const void* v, int64_t tokens, int32_t q_heads,
+                        int32_t kv_heads, int32_t dim, int32_t dtype, int64_t q_token_stride,
+                        int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                        int64_t v_token_stride, int64_t v_head_stride, const void* positions,
+                        int32_t axes, const uint8_t* pair_axes, int32_t index_type, const float* cos_sin,
+                        int64_t places, int32_t rot_dim, int32_t interleaved, int32_t norm,
+                        const void* q_weight, const void* k_weight, float eps, void* q_out, void* k_out,
+                        void* k_pages, void* v_pages, const int64_t* slots, int64_t pages,
+                        int32_t page_size, int32_t bits, int32_t* err_count, qemb_stream_t stream) {
   if (tokens < 0 || places < 0 || pages < 0 || rot_dim < 0 || rot_dim > dim) return QEMB_E_INVALID_ARG;
+  if (axes < 1 || axes > QEMB_MAX_AXES || (axes > 1 && rot_dim && !pair_axes) || (!norm && (q_weight || k_weight))) return QEMB_E_INVALID_ARG;
   if (index_type != QEMB_INDEX_INT32 && index_type != QEMB_INDEX_INT64) return QEMB_E_INVALID_ARG;
   if (int rc = check_heads(q_heads, kv_heads, dim, dtype)) return rc;
   if (rot_dim % 16) return QEMB_E_UNSUPPORTED;
@@ -97,6 +100,7 @@ int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, 
   for (const void* p : {q, k, (const void*)(cached ? v : nullptr), (const void*)q_out, (const void*)k_out,
                         (const void*)k_pages, (const void*)v_pages, (const void*)cos_sin, q_weight, k_weight})
     if (!aligned(p, 16)) return QEMB_E_MISALIGNED;
+  if (!aligned(pair_axes, 4)) return QEMB_E_MISALIGNED;
   if (!aligned(positions, index_type == QEMB_INDEX_INT64 ? 8 : 4) || !aligned(slots, 8)) return QEMB_E_MISALIGNED;
   NormRopeArgs a;
   a.x[0] = q, a.x[1] = k, a.x[2] = v;
@@ -109,6 +113,7 @@ int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, 
   a.q_heads = q_heads, a.kv_heads = kv_heads, a.dim = dim;
   a.rows = q_heads + (cached ? 2 : 1) * kv_heads;
   a.positions = positions, a.idx64 = index_type == QEMB_INDEX_INT64;
+  a.axes = axes, a.pair_axes = pair_axes, a.norm = norm != 0;
   a.cos_sin = cos_sin, a.places = places, a.rot = rot_dim, a.interleaved = interleaved != 0;
   a.eps = eps;
   a.slots = cached ? slots : nullptr;
@@ -116,8 +121,26 @@ int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, 
   a.row_bytes = cached ? row_bytes_of(dim, bits) : 0;
   a.err_count = err_count;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  return dtype == QEMB_DTYPE_BF16 ? launch_norm_rope<__bf16>(a, cached ? bits : 16, st)
-                                  : launch_norm_rope<_Float16>(a, cached ? bits : 16, st);
+  const int row_bits = cached ? bits : 16;
+  // one axis with a norm keeps the kernel that loads its angles in whole pieces
+  const bool plain = axes == 1 && !pair_axes && norm;
+  if (dtype == QEMB_DTYPE_BF16) return plain ? launch_norm_rope<__bf16, false>(a, row_bits, st) : launch_norm_rope<__bf16, true>(a, row_bits, st);
+  return plain ? launch_norm_rope<_Float16, false>(a, row_bits, st) : launch_norm_rope<_Float16, true>(a, row_bits, st);
+}
+
+int qemb_norm_rope(const void* q, const void* k, const void* v, int64_t tokens, int32_t q_heads,
+                   int32_t kv_heads, int32_t dim, int32_t dtype, int64_t q_token_stride,
+                   int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                   int64_t v_token_stride, int64_t v_head_stride, const void* positions,
+                   int32_t index_type, const float* cos_sin, int64_t places, int32_t rot_dim,
+                   int32_t interleaved, const void* q_weight, const void* k_weight, float eps,
+                   void* q_out, void* k_out, void* k_pages, void* v_pages, const int64_t* slots,
+                   int64_t pages, int32_t page_size, int32_t bits, int32_t* err_count,
+                   qemb_stream_t stream) {
+  return qemb_norm_rope_axes(q, k, v, tokens, q_heads, kv_heads, dim, dtype, q_token_stride, q_head_stride, k_token_stride,
+                             k_head_stride, v_token_stride, v_head_stride, positions, 1, nullptr, index_type, cos_sin, places,
+                             rot_dim, interleaved, 1, q_weight, k_weight, eps, q_out, k_out, k_pages, v_pages, slots, pages,
+                             page_size, bits, err_count, stream);
 }
 
 int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q_tokens,
@@ -204,6 +227,52 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
   a.out = out, a.lse = lse, a.workspace = (float*)workspace, a.err_count = err_count;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   return dtype == QEMB_DTYPE_BF16 ? launch_decode<__bf16>(a, plan, bits, st) : launch_decode<_Float16>(a, plan, bits, st);
+}
+
+size_t qemb_shared_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t groups,
+                                   int32_t prefix_width, int32_t width, int32_t page_size) {
+  if (batch < 1 || check_groups(q_heads, kv_heads, dim, QEMB_DTYPE_BF16) != QEMB_OK || groups < 1 || prefix_width < 0 || width < 0 ||
+      !is_pow2(page_size) || (int64_t)width * page_size > kMostPlaces || (int64_t)prefix_width * page_size > kMostPlaces)
+    return 0;
+  return shared_plan(batch, q_heads, kv_heads, dim, groups, (int64_t)prefix_width * page_size, (int64_t)width * page_size).bytes;
+}
+
+int qemb_shared_attention(const void* q, const void* k_pages, const void* v_pages, int64_t pages, int32_t page_size,
+                          int32_t bits, int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t dtype,
+                          const int32_t* prefix_table, int32_t prefix_width, const int32_t* prefix_lens,
+                          const int32_t* group_offsets, int32_t groups, const int32_t* block_table, int32_t width,
+                          const int32_t* seq_lens, float scale, void* out, float* lse, void* workspace,
+                          int32_t* err_count, qemb_stream_t stream) {
+  if (batch < 0 || width < 0 || prefix_width < 0 || pages < 0 || groups < 1 || !is_pow2(page_size)) return QEMB_E_INVALID_ARG;
+  if (!isfinite(scale) || (groups > 1 && !group_offsets)) return QEMB_E_INVALID_ARG;
+  if (bits != 16 && bits != 8 && bits != 4) return QEMB_E_INVALID_ARG;
+  if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
+  if ((int64_t)width * page_size > kMostPlaces || (int64_t)prefix_width * page_size > kMostPlaces) return QEMB_E_UNSUPPORTED;
+  if ((int64_t)batch * q_heads > kMostPlaces) return QEMB_E_UNSUPPORTED;
+  if ((int64_t)kv_heads * page_size > INT32_MAX || (int64_t)kv_heads * page_size * row_bytes_of(dim, bits) > INT32_MAX)
+    return QEMB_E_UNSUPPORTED;  // a page's bytes are counted in 32 bits
+  if (batch == 0) return QEMB_OK;
+  if (!q || !out || !seq_lens || !prefix_lens || (width > 0 && !block_table) || (prefix_width > 0 && !prefix_table) ||
+      (pages > 0 && (!k_pages || !v_pages)))
+    return QEMB_E_INVALID_ARG;
+  for (const void* p : {q, k_pages, v_pages, (const void*)out, (const void*)workspace})
+    if (!aligned(p, 16)) return QEMB_E_MISALIGNED;
+  for (const void* p : {(const void*)block_table, (const void*)seq_lens, (const void*)prefix_table, (const void*)prefix_lens,
+                        (const void*)group_offsets, (const void*)lse})
+    if (!aligned(p, 4)) return QEMB_E_MISALIGNED;
+  const SharedPlan plan = shared_plan(batch, q_heads, kv_heads, dim, groups, (int64_t)prefix_width * page_size, (int64_t)width * page_size);
+  if (plan.bytes && !workspace) return QEMB_E_INVALID_ARG;
+  SharedArgs a;
+  a.q = q;
+  a.pages[0] = k_pages, a.pages[1] = v_pages;
+  a.n_pages = pages, a.page_log2 = log2_of(page_size), a.row_bytes = row_bytes_of(dim, bits);
+  a.batch = batch, a.q_heads = q_heads, a.kv_heads = kv_heads, a.dim = dim, a.groups = groups;
+  a.prefix_table = prefix_table, a.prefix_width = prefix_width, a.prefix_lens = prefix_lens;
+  a.group_offsets = group_offsets, a.block_table = block_table, a.width = width, a.seq_lens = seq_lens;
+  a.scale = scale;
+  a.out = out, a.lse = lse, a.workspace = (float*)workspace, a.err_count = err_count;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  return dtype == QEMB_DTYPE_BF16 ? launch_shared<__bf16>(a, plan, bits, st) : launch_shared<_Float16>(a, plan, bits, st);
 }
 
 int qemb_evict(const void* k_pages, const void* v_pages, int64_t pages, int32_t page_size,
