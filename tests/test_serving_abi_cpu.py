@@ -95,7 +95,7 @@ SHARED = dict(q=FAKE, k=FAKE, v=FAKE, pages=9, page=16, bits=16, batch=3, hq=4, 
     (dict(page=1024, width=2 ** 21), -3), (dict(page=1024, prefix_width=2 ** 21), -3), (dict(page=1, prefix_width=MOST), -3), (dict(batch=MOST, hq=2, hkv=1), -3),
     (dict(page=2 ** 26, width=1, prefix_width=1), -3), (dict(scale=float("nan")), -1), (dict(scale=-float("inf")), -1),
     (dict(q=None), -1), (dict(k=None), -1), (dict(v=None), -1), (dict(out=None), -1), (dict(lens=None), -1), (dict(prefix_lens=None), -1),
-    (dict(table=None), -1), (dict(prefix=None), -1), (dict(q=MIS), -2), (dict(k=MIS), -2), (dict(out=MIS), -2), (dict(ws=MIS), -2),
+    (dict(table=None), -1), (dict(prefix=None), -1), (dict(ws=None), -1), (dict(q=MIS), -2), (dict(k=MIS), -2), (dict(out=MIS), -2), (dict(ws=MIS), -2),
     (dict(table=MIS), -2), (dict(prefix=MIS), -2), (dict(prefix_lens=MIS), -2), (dict(offsets=MIS), -2), (dict(lens=MIS), -2), (dict(lse=MIS), -2),
     (dict(batch=0, q=None), 0),
 ])
@@ -106,6 +106,7 @@ def test_shared_refusals(attention_lib, change, rc):  # noqa: F811
 def test_shared_workspace(attention_lib):  # noqa: F811
     w = attention_lib.qemb_shared_workspace_bytes
     #      batch hq hkv dim groups prefix_width width page
+    assert w(3, 4, 2, 64, 2, 8, 4, 16) > 0
     for bad in ((0, 4, 2, 64, 1, 8, 4, 16), (3, 5, 2, 64, 1, 8, 4, 16), (3, 4, 2, 64, 0, 8, 4, 16), (3, 4, 2, 64, 1, -1, 4, 16), (3, 4, 2, 64, 1, 8, -1, 16),
                 (3, 4, 2, 64, 1, 8, 4, 15), (3, 4, 2, 64, 1, 2 ** 27, 4, 16)):
         assert w(*bad) == 0
