@@ -60,6 +60,7 @@ LOGPROBS = dict(logits=FAKE, rows=4, vocab=1000, dtype=0, stride=1000, targets=F
     (dict(logprobs=None), -1), (dict(ids=None), -1), (dict(tops=None), -1), (dict(logits=FAKE + 1), -2), (dict(logits=MIS, dtype=2), -2),
     (dict(targets=FAKE + 4), -2), (dict(targets=MIS, itype=0), -2), (dict(logprobs=MIS), -2), (dict(entropy=MIS), -2), (dict(lse=MIS), -2),
     (dict(ids=MIS), -2), (dict(tops=MIS), -2), (dict(ws=FAKE + 8), -2), (dict(rows=0, logits=None), 0),
+    (dict(rows=1, vocab=200000, ws=None), -1),
 ])
 def test_logprobs_refusals(lib, change, rc):
     assert call(lib.qemb_token_logprobs, LOGPROBS, **change) == rc
@@ -67,6 +68,7 @@ def test_logprobs_refusals(lib, change, rc):
 
 def test_logprobs_workspace(lib):
     w = lib.qemb_logprobs_workspace_bytes
+    assert w(1, 200000, 0, 20) > 0
     for bad in ((0, 1000, 0, 5), (4, 0, 0, 5), (4, 2 ** 30 + 1, 0, 5), (4, 1000, 3, 5), (4, 1000, 0, 65), (4, 1000, 0, -1)):
         assert w(*bad) == 0
     assert w(2 ** 24 - 1, 2 ** 30, 2, 64) < 2 ** 50  # no overflow at the largest sizes
