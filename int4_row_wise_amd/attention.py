@@ -393,7 +393,7 @@ def shared_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     elif groups != 1:
         raise ValueError("%d prefixes need group_offsets" % groups)
     if out is None:
-        out = torch.empty((b, hq, d), dtype=dtype, device=q.device)
+        out = q.new_empty((b, hq, d))
     else:
         _want("out", out, (b, hq, d), dtype, dev)
     if lse is not None:
@@ -407,7 +407,7 @@ def shared_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
             raise ValueError("workspace must have at least %d bytes" % need)
         _want("workspace", workspace, workspace.shape, torch.uint8, dev)
     elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     _check("qemb_shared_attention", L.qemb_shared_attention(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages, size, bits, b, hq, hkv, d, _DTYPES[dtype],
         prefix_table.data_ptr(), prefix_width, prefix_lens.data_ptr(), _ptr(group_offsets), groups,

@@ -98,7 +98,7 @@ def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weight: O
     else:
         want, kind = (n, d), kind or dtype
     if out is None:
-        out = torch.empty(want, dtype=kind, device=x.device)
+        out = x.new_empty(want, dtype=kind)
     else:
         _want("out", out, want, kind, dev)
     if code == 1 or code == 2:
@@ -106,7 +106,7 @@ def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weight: O
             raise ValueError("group must divide the rows' %d elements, got %d" % (d, group))
         of_scales = (n, d // group) if group else (n,)
         if scales is None:
-            scales = torch.empty(of_scales, dtype=torch.float32, device=x.device)
+            scales = x.new_empty(of_scales, dtype=torch.float32)
         else:
             _want("scales", scales, of_scales, torch.float32, dev)
     elif scales is not None or group:
@@ -114,7 +114,7 @@ def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weight: O
     if sum_out is not None:
         ss = _rows("sum_out", sum_out, shape, dtype, dev)
     elif residual is not None:
-        sum_out, ss = torch.empty(shape, dtype=dtype, device=x.device), d
+        sum_out, ss = x.new_empty(shape), d
     else:
         ss = 0
     _check("qemb_add_norm", load_serving_library().qemb_add_norm(
@@ -152,11 +152,11 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     if targets is not None:
         wide = isinstance(targets, torch.Tensor) and targets.dtype is torch.int64
         _want("targets", targets, (n,), torch.int64 if wide else torch.int32, dev)
-        logprobs = torch.empty(n, dtype=torch.float32, device=logits.device)
-    entropy = torch.empty(n, dtype=torch.float32, device=logits.device)
+        logprobs = logits.new_empty(n, dtype=torch.float32)
+    entropy = logits.new_empty(n, dtype=torch.float32)
     if top:
-        ids = torch.empty((n, top), dtype=torch.int32, device=logits.device)
-        tops = torch.empty((n, top), dtype=torch.float32, device=logits.device)
+        ids = logits.new_empty((n, top), dtype=torch.int32)
+        tops = logits.new_empty((n, top), dtype=torch.float32)
     if lse is not None:
         _want("lse", lse, (n,), torch.float32, dev)
     if err_count is not None:
@@ -168,7 +168,7 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
             raise ValueError("workspace must have at least %d bytes" % need)
         _want("workspace", workspace, workspace.shape, torch.uint8, dev)
     elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+        workspace = logits.new_empty(need, dtype=torch.uint8)
     _check("qemb_token_logprobs", L.qemb_token_logprobs(
         logits.data_ptr(), n, v, _DTYPES[dtype], stride, _ptr(targets), INDEX_INT64 if wide else INDEX_INT32, top,
         _ptr(logprobs), entropy.data_ptr(), _ptr(lse), _ptr(ids), _ptr(tops), _ptr(workspace), _ptr(err_count),
