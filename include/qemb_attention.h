@@ -206,7 +206,7 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
  * width * page_size and prefix_width * page_size: at most 2^31 - 1024.
  */
 size_t qemb_shared_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t groups,
-                                   int32_t prefix_width, int32_t width, int32_t page_size);
+                                   int32_t prefix_width, int32_t width, int32_t page_size, int32_t bits);
 
 int qemb_shared_attention(const void* q, const void* k_pages, const void* v_pages, int64_t pages,
                           int32_t page_size, int32_t bits, int32_t batch, int32_t q_heads,

@@ -67,7 +67,7 @@ def load_attention_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.qemb_decode_attention.argtypes = [p, p, p, i64, i32, i32, i32, i32, i32, i32, i32, p, i32, p, i32, i32, f32,
                                         p, i64, p, p, p, p, p]
     L.qemb_decode_attention.restype = ctypes.c_int
-    L.qemb_shared_workspace_bytes.argtypes = [i32] * 8
+    L.qemb_shared_workspace_bytes.argtypes = [i32] * 9
     L.qemb_shared_workspace_bytes.restype = ctypes.c_size_t
     L.qemb_shared_attention.argtypes = [p, p, p, i64, i32, i32, i32, i32, i32, i32, i32, p, i32, p, p, i32, p, i32, p,
                                         f32, p, p, p, p, p]
@@ -350,13 +350,14 @@ def decode_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
 
 
 def shared_workspace_bytes(batch: int, q_heads: int, kv_heads: int, dim: int, groups: int, prefix_width: int, width: int,
-                           page_size: int) -> int:
+                           page_size: int, bits: int = 16) -> int:
     """Bytes of workspace that shared_attention needs for these sizes."""
     for name, value in (("batch", batch), ("q_heads", q_heads), ("kv_heads", kv_heads), ("dim", dim), ("groups", groups),
-                        ("prefix_width", prefix_width), ("width", width), ("page_size", page_size)):
+                        ("prefix_width", prefix_width), ("width", width), ("page_size", page_size),
+                        ("bits", bits)):
         _int32(name, value)
     return int(load_attention_library().qemb_shared_workspace_bytes(
-        batch, q_heads, kv_heads, dim, groups, prefix_width, width, page_size))
+        batch, q_heads, kv_heads, dim, groups, prefix_width, width, page_size, bits))
 
 
 def shared_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, prefix_table: torch.Tensor,
@@ -401,7 +402,7 @@ def shared_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     if err_count is not None:
         _want("err_count", err_count, (1,), torch.int32, dev)
     L = load_attention_library()
-    need = L.qemb_shared_workspace_bytes(b, hq, hkv, d, groups, prefix_width, width, size)
+    need = L.qemb_shared_workspace_bytes(b, hq, hkv, d, groups, prefix_width, width, size, bits)
     if workspace is not None:
         if workspace.numel() < need:
             raise ValueError("workspace must have at least %d bytes" % need)

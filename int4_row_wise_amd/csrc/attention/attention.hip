@@ -230,11 +230,11 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
 }
 
 size_t qemb_shared_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t groups,
-                                   int32_t prefix_width, int32_t width, int32_t page_size) {
-  if (batch < 1 || check_groups(q_heads, kv_heads, dim, QEMB_DTYPE_BF16) != QEMB_OK || groups < 1 || prefix_width < 0 || width < 0 ||
+                                   int32_t prefix_width, int32_t width, int32_t page_size, int32_t bits) {
+  if (batch < 1 || (bits != 16 && bits != 8 && bits != 4) || check_groups(q_heads, kv_heads, dim, QEMB_DTYPE_BF16) != QEMB_OK || groups < 1 || prefix_width < 0 || width < 0 ||
       !is_pow2(page_size) || (int64_t)width * page_size > kMostPlaces || (int64_t)prefix_width * page_size > kMostPlaces)
     return 0;
-  return shared_plan(batch, q_heads, kv_heads, dim, groups, (int64_t)prefix_width * page_size, (int64_t)width * page_size).bytes;
+  return shared_plan(batch, q_heads, kv_heads, dim, groups, (int64_t)prefix_width * page_size, (int64_t)width * page_size, bits).bytes;
 }
 
 int qemb_shared_attention(const void* q, const void* k_pages, const void* v_pages, int64_t pages, int32_t page_size,
@@ -260,8 +260,8 @@ int qemb_shared_attention(const void* q, const void* k_pages, const void* v_page
   for (const void* p : {(const void*)block_table, (const void*)seq_lens, (const void*)prefix_table, (const void*)prefix_lens,
                         (const void*)group_offsets, (const void*)lse})
     if (!aligned(p, 4)) return QEMB_E_MISALIGNED;
-  const SharedPlan plan = shared_plan(batch, q_heads, kv_heads, dim, groups, (int64_t)prefix_width * page_size, (int64_t)width * page_size);
-  if (plan.bytes && !workspace) return QEMB_E_INVALID_ARG;
+  const SharedPlan plan = shared_plan(batch, q_heads, kv_heads, dim, groups, (int64_t)prefix_width * page_size, (int64_t)width * page_size, bits);
+  if (!workspace) return QEMB_E_INVALID_ARG;
   SharedArgs a;
   a.q = q;
   a.pages[0] = k_pages, a.pages[1] = v_pages;

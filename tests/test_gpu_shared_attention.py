@@ -102,7 +102,7 @@ def test_heads(q, bits, heads):
 
 
 @pytest.mark.parametrize("bits", [16, 8])
-@pytest.mark.parametrize("size", [1, 4, 5, 8, 16, 31, 32, 33, 40, 64, 65, 129])
+@pytest.mark.parametrize("size", [1, 2, 3, 4, 5, 8, 11, 12, 13, 16, 31, 32, 33, 40, 64, 65, 129])
 def test_group_sizes(q, size, bits):
     """Rows of a group around the tiles that share a prefix (4 query heads a kv head)."""
     g = np.random.default_rng(2200 + size)
@@ -123,7 +123,7 @@ def test_prefix_lengths(q, n):
 @pytest.mark.parametrize("bits", [16, 8, 4])
 def test_pages_that_end_inside_a_tile(q, page, bits):
     g = np.random.default_rng(2400 + page)
-    for size in (3, 20):
+    for size in (3, 20):  # packed: tiles of 16 rows, and wide ones
         cache = Shared(g, q, [size], [301], [int(n) for n in g.integers(0, 100, size)], 2, 128, bits, page, "bf16")
         cache.poison_unowned(float("nan") if bits == 16 else 255)
         check(q, g, cache, 8, "bf16", rows=50)
@@ -373,7 +373,7 @@ def test_workspace_is_enough_and_not_left(q):
     for sizes, prefixes, hq, bits in (([40], [2000], 8, 16), ([2], [5000], 4, 8), ([3, 0, 70], [900, 5, 40], 6, 4), ([1], [1], 2, 16)):
         b = sum(sizes)
         cache = Shared(g, q, sizes, prefixes, [int(n) for n in g.integers(0, 700, b)], 2, 64, bits, 16, "bf16")
-        need = q.shared_workspace_bytes(b, hq, 2, 64, len(sizes), cache.prefix_table.shape[1], cache.block_table.shape[1], 16)
+        need = q.shared_workspace_bytes(b, hq, 2, 64, len(sizes), cache.prefix_table.shape[1], cache.block_table.shape[1], 16, bits)
         room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
         qt, _ = rand16(g, (b, hq, 64), "bf16")
         want = cache.call(q, qt)
@@ -390,7 +390,7 @@ def test_two_graphs_share_a_workspace(q):
     g = np.random.default_rng(2780)
     caches = [Shared(g, q, [30], [1500], [int(n) for n in g.integers(0, 600, 30)], 2, 64, 16, 16, "bf16"),
               Shared(g, q, [2, 1], [700, 80], [20, 0, 300], 2, 64, 8, 16, "bf16")]
-    room = torch.empty(max(q.shared_workspace_bytes(c.batch, 8, 2, 64, c.n_groups, c.prefix_table.shape[1], c.block_table.shape[1], 16) for c in caches),
+    room = torch.empty(max(q.shared_workspace_bytes(c.batch, 8, 2, 64, c.n_groups, c.prefix_table.shape[1], c.block_table.shape[1], 16, c.bits) for c in caches),
                        dtype=torch.uint8, device="cuda")
     inputs = [torch.zeros((c.batch, 8, 64), dtype=torch.bfloat16, device="cuda") for c in caches]
     lses = [torch.zeros((c.batch, 8), device="cuda") for c in caches]

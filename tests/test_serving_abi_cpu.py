@@ -107,10 +107,10 @@ def test_shared_refusals(attention_lib, change, rc):  # noqa: F811
 
 def test_shared_workspace(attention_lib):  # noqa: F811
     w = attention_lib.qemb_shared_workspace_bytes
-    #      batch hq hkv dim groups prefix_width width page
-    assert w(3, 4, 2, 64, 2, 8, 4, 16) > 0
-    for bad in ((0, 4, 2, 64, 1, 8, 4, 16), (3, 5, 2, 64, 1, 8, 4, 16), (3, 4, 2, 64, 0, 8, 4, 16), (3, 4, 2, 64, 1, -1, 4, 16), (3, 4, 2, 64, 1, 8, -1, 16),
-                (3, 4, 2, 64, 1, 8, 4, 15), (3, 4, 2, 64, 1, 2 ** 27, 4, 16)):
+    #      batch hq hkv dim groups prefix_width width page bits
+    assert w(3, 4, 2, 64, 2, 8, 4, 16, 16) > 0
+    for bad in ((0, 4, 2, 64, 1, 8, 4, 16, 16), (3, 5, 2, 64, 1, 8, 4, 16, 16), (3, 4, 2, 64, 0, 8, 4, 16, 16), (3, 4, 2, 64, 1, -1, 4, 16, 16),
+                (3, 4, 2, 64, 1, 8, -1, 16, 16), (3, 4, 2, 64, 1, 8, 4, 15, 16), (3, 4, 2, 64, 1, 2 ** 27, 4, 16, 16), (3, 4, 2, 64, 1, 8, 4, 16, 5)):
         assert w(*bad) == 0
 
 
