@@ -90,6 +90,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _launch(dev: int, fn, *args) -> int:
+    """Calls fn(*args) with the tensors' GPU as the current one: kernels are launched there."""
+    if dev == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _device(name: str, t: torch.Tensor) -> int:
     """The GPU index of the tensor that decides where a call runs."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -228,7 +236,8 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin
             _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(slots),
             pages, size, bits, _ptr(err_count), _raw_stream(dev)))
     else:
-        _check("qemb_norm_rope_axes", load_attention_library().qemb_norm_rope_axes(
+        _check("qemb_norm_rope_axes", _launch(
+            dev, load_attention_library().qemb_norm_rope_axes,
             q.data_ptr(), k.data_ptr(), _ptr(v), n, hq, hkv, d, _DTYPES[dtype], qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
             positions.data_ptr(), axes, _ptr(pair_axes), index, cos_sin.data_ptr(), places, rot, int(interleaved), int(norm),
             _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(slots),
@@ -409,7 +418,8 @@ def shared_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
         _want("workspace", workspace, workspace.shape, torch.uint8, dev)
     elif need:
         workspace = q.new_empty(need, dtype=torch.uint8)
-    _check("qemb_shared_attention", L.qemb_shared_attention(
+    _check("qemb_shared_attention", _launch(
+        dev, L.qemb_shared_attention,
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages, size, bits, b, hq, hkv, d, _DTYPES[dtype],
         prefix_table.data_ptr(), prefix_width, prefix_lens.data_ptr(), _ptr(group_offsets), groups,
         block_table.data_ptr(), width, seq_lens.data_ptr(), d ** -0.5 if scale is None else scale, out.data_ptr(),

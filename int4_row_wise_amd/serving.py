@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .attention import _check, _device, _raw_stream, _want
+from .attention import _check, _device, _launch, _raw_stream, _want
 from .qemb import INDEX_INT32, INDEX_INT64, QembError, _ptr
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -117,7 +117,8 @@ def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weight: O
         sum_out, ss = x.new_empty(shape), d
     else:
         ss = 0
-    _check("qemb_add_norm", load_serving_library().qemb_add_norm(
+    _check("qemb_add_norm", _launch(
+        dev, load_serving_library().qemb_add_norm,
         x.data_ptr(), _ptr(residual), _ptr(weight), n, d, _DTYPES[dtype], xs, rs, ss, eps, code, group, out.data_ptr(),
         _ptr(scales), _ptr(sum_out), _raw_stream(dev)))
     return out, sum_out, scales
@@ -169,7 +170,8 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
         _want("workspace", workspace, workspace.shape, torch.uint8, dev)
     elif need:
         workspace = logits.new_empty(need, dtype=torch.uint8)
-    _check("qemb_token_logprobs", L.qemb_token_logprobs(
+    _check("qemb_token_logprobs", _launch(
+        dev, L.qemb_token_logprobs,
         logits.data_ptr(), n, v, _DTYPES[dtype], stride, _ptr(targets), INDEX_INT64 if wide else INDEX_INT32, top,
         _ptr(logprobs), entropy.data_ptr(), _ptr(lse), _ptr(ids), _ptr(tops), _ptr(workspace), _ptr(err_count),
         _raw_stream(dev)))

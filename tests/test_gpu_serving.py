@@ -471,3 +471,55 @@ def test_logprobs_empty_and_refusals(q):
     ):
         with pytest.raises(error):
             q.token_logprobs(*args, **more)
+
+
+def test_logprobs_any_nan_is_passed_over(q):
+    """NaN of every kind (quiet or not, of either sign) beside large logits: the ids stand."""
+    import torch
+    g = np.random.default_rng(6000)
+    for v in (700, 20000):
+        x = (g.standard_normal((4, v)) * 2).astype(np.float32)
+        for dtype, kind, bits in ((torch.bfloat16, torch.int16, (0x7F81, -0x7F, 0x7FC0, -0x40)), (torch.float16, torch.int16, (0x7C01, -0x3FF, 0x7E00, -0x200)),
+                                  (torch.float32, torch.int32, (0x7F800001, -0x7FFFFF, 0x7FC00000, -0x400000))):
+            t = torch.from_numpy(x).to(dtype)
+            places = g.choice(v, 60, replace=False)
+            raw = t.view(kind)
+            for i, at in enumerate(places):
+                raw[i % 4, int(at)] = bits[i // 4 % 4]
+            xv = t.double().numpy()
+            assert np.isnan(xv).sum() == 60
+            _, ent, ids, tops = q.token_logprobs(t.cuda(), top=12)
+            assert np.isnan(f64(ent)).all() and np.isnan(f64(tops)).all()
+            for i in range(4):
+                order = np.lexsort((np.arange(v), -np.where(np.isnan(xv[i]), -np.inf, xv[i])))[:12]
+                assert np.array_equal(host(ids)[i], order), (dtype, v, i)
+
+
+def test_logprobs_largest_at_every_place(q):
+    """One logit above all others, at every border of vectors, slices, chunks and parts."""
+    import torch
+    v = 40001
+    for dtype in (torch.bfloat16, torch.float32):
+        each = 8 if dtype is torch.bfloat16 else 4
+        places = sorted({p for base in (0, each, 64 * each, 256 * each, 512 * each, 1024 * each, 2048 * each, v) for p in (base - 1, base, base + 1) if 0 <= p < v})
+        x = torch.zeros((len(places), v), dtype=dtype, device="cuda")
+        at = torch.tensor(places, device="cuda")
+        x[torch.arange(len(places)), at] = 9.0
+        lp, ent, ids, tops = q.token_logprobs(x, at, top=2)
+        want = 9.0 - np.log(np.exp(9.0) + v - 1)
+        assert torch.equal(ids[:, 0], at.int()) and ids[:, 1].tolist() == [1 if p == 0 else 0 for p in places]
+        assert float((lp - want).abs().max()) < 1e-4 and torch.equal(lp, tops[:, 0])
+
+
+def test_logprobs_rising_and_falling_rows(q):
+    """Rows whose largest logits come last, or all in one thread's vectors, so that bounds keep moving."""
+    g = np.random.default_rng(6100)
+    import torch
+    v = 60000
+    x = np.stack([np.arange(v) * 1e-3, np.arange(v)[::-1] * 1e-3, np.where(np.arange(v) % 2048 < 8, 5.0, 0.0) + np.arange(v) * 1e-6,
+                  np.repeat(np.arange(v // 100), 100) * 0.05]).astype(np.float32)
+    for top in (1, 20, 64):
+        t = torch.from_numpy(x)
+        check_logprobs(q, t.cuda(), t.double().numpy(), [int(i) for i in g.integers(0, v, 4)], top, "rising")
+        t = t.bfloat16()
+        check_logprobs(q, t.cuda(), t.double().numpy(), [int(i) for i in g.integers(0, v, 4)], top, "rising, 16 bits")

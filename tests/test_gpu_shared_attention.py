@@ -454,3 +454,75 @@ def test_refusals(q):
     with pytest.raises(ValueError):
         q.shared_attention(qt, c.pool[0], c.pool[1], c.prefix_table, c.prefix_lens, c.block_table[:3], c.own_lens)
     assert host(c.own_lens).tolist() == [5] * 4
+
+
+@pytest.mark.parametrize("page", [4, 16, 64])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_rows_of_bad_pages_are_left_out(q, bits, page):
+    """In the prefix and among a sequence's own rows, against float64 without those rows."""
+    import torch
+    g = np.random.default_rng(2800 + page + bits)
+    for size in (2, 40):
+        cache = Shared(g, q, [size], [500], [150 + i for i in range(size)], 1, 64, bits, page, "bf16")
+        bad = {0: 3, 1: 1}  # a page of the prefix, and one of the first sequence
+        for row, at in bad.items():
+            (cache.prefix_table if row == 0 else cache.block_table)[0, at] = 2 ** 31 - 1 - row
+        qt, qv = rand16(g, (size, 4, 64), "bf16")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        lse = torch.zeros((size, 4), device="cuda")
+        out = cache.call(q, qt, err_count=err, lse=lse)
+        assert int(err[0]) >= 1
+        for b in (0, size - 1):
+            k, kr = cache.seen(0, b, 0)
+            v, vr = cache.seen(1, b, 0)
+            see = np.ones(len(k), bool)
+            see[3 * page:4 * page] = False
+            if b == 0:
+                see[500 + page:500 + 2 * page] = False
+            for h in range(4):
+                o, ob, ls, lb, _, _ = model.attend(qv[b, h], k, v, see, 64 ** -0.5, "bf16", kr, vr)
+                close(f64(out)[b, h], o, ob, "out")
+                close(f64(lse)[b, h], ls, lb, "lse")
+
+
+def test_bad_offsets_among_many_groups(q):
+    """A fall beyond the 64th group is found, too."""
+    import torch
+    g = np.random.default_rng(2810)
+    sizes = [1] * 80
+    cache = Shared(g, q, sizes, [20] * 80, [5] * 80, 1, 64, 16, 4, "bf16")
+    qt, _ = rand16(g, (80, 2, 64), "bf16")
+    off = cache.offsets.clone()
+    off[70] = 3
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = cache.call(q, qt, group_offsets=off, err_count=err)
+    assert int(err[0]) == 1
+    alone = q.decode_attention(qt, cache.pool[0], cache.pool[1], cache.block_table, cache.own_lens)
+    assert float((out.double() - alone.double()).norm() / alone.double().norm()) < 2 * 2.0 ** -8
+
+
+def test_two_calls_at_once(q):
+    """On two streams, each with the workspace of its own call."""
+    import torch
+    g = np.random.default_rng(2820)
+    caches = [Shared(g, q, [60], [4000], [50] * 60, 2, 64, bits, 16, "bf16") for bits in (16, 8)]
+    qs = [rand16(g, (60, 8, 64), "bf16")[0] for _ in caches]
+    want = [c.call(q, x) for c, x in zip(caches, qs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in caches]
+    got = [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(caches[i].call(q, qs[i]))
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in outs)
+
+
+def test_prefixes_of_very_different_lengths(q):
+    """Shares of the work that groups take from each other; one group with nearly all of it."""
+    g = np.random.default_rng(2830)
+    for sizes, prefixes, bits in (([1, 1, 1, 60], [30000, 3, 40, 130], 16), ([100, 2], [64, 20000], 8), ([2, 0, 3, 0, 1], [0, 5000, 9000, 1, 129], 4)):
+        cache = Shared(g, q, sizes, prefixes, [int(n) for n in g.integers(0, 70, sum(sizes))], 2, 64, bits, 16, "bf16")
+        check(q, g, cache, 8, "bf16", rows=40)

@@ -140,3 +140,21 @@ def test_library_from_other_sources_is_refused(lib, tmp_path, monkeypatch):
     with pytest.raises(serving.QembError, match="not built"):
         serving.load_serving_library(str(stale))
     assert isinstance(serving.load_serving_library(), ctypes.CDLL)
+
+
+def test_launches_make_the_tensors_gpu_current(monkeypatch):
+    """A call for another GPU than the current one runs with that one current, and only such a call."""
+    import contextlib
+
+    from int4_row_wise_amd import attention
+    entered = []
+
+    @contextlib.contextmanager
+    def device(index):
+        entered.append(index)
+        yield
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    assert attention._launch(0, lambda *a: sum(a), 1, 2) == 3 and entered == []
+    assert attention._launch(2, lambda *a: sum(a), 1, 2) == 3 and entered == [2]
