@@ -186,8 +186,8 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
  * the pages prefix_table[g] and then its sequence's own seq_lens[b] rows of the
  * pages block_table[b] (its own row among them):
  *     out = sum_j softmax_j(scale q.k_j) v_j,  lse = log sum_j exp(scale q.k_j)
- * Equal rows give the bits of the same sums in another order than
- * qemb_decode_attention's.
+ * The sums run in another order than qemb_decode_attention's: over the same rows the
+ * last bits may differ.
  *   q, k_pages, v_pages, block_table [batch][width], seq_lens  as in
  *                qemb_decode_attention; a length may be 0 here
  *   prefix_table [groups][prefix_width] int32, prefix_lens [groups] int32, each
