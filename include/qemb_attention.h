@@ -199,9 +199,10 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
  *                contents need not be kept
  * A sequence that no group holds sees its own rows alone; one that sees nothing
  * gives zeros and lse = -inf.  A length that leaves its range is taken as 0 and
- * counted.  Offsets that decrease anywhere or leave [0, batch] make no groups
- * (every sequence as if no group held it) and are counted once.  The rows of a
- * page outside [0, pages) are taken as not
+ * counted, once each: a prefix's also where its group has no sequences or the
+ * offsets make no groups.  Offsets that decrease anywhere or leave [0, batch] make
+ * no groups (every sequence as if no group held it) and are counted once.  The
+ * rows of a page outside [0, pages) that some sequence would see are taken as not
  * visible and counted (at least once).
  * width * page_size and prefix_width * page_size: at most 2^31 - 1024.
  */

@@ -526,3 +526,30 @@ def test_prefixes_of_very_different_lengths(q):
     for sizes, prefixes, bits in (([1, 1, 1, 60], [30000, 3, 40, 130], 16), ([100, 2], [64, 20000], 8), ([2, 0, 3, 0, 1], [0, 5000, 9000, 1, 129], 4)):
         cache = Shared(g, q, sizes, prefixes, [int(n) for n in g.integers(0, 70, sum(sizes))], 2, 64, bits, 16, "bf16")
         check(q, g, cache, 8, "bf16", rows=40)
+
+
+@pytest.mark.parametrize("groups", [4, 70])
+def test_every_bad_prefix_length_is_counted(q, groups):
+    """Those of groups without sequences, and those beside offsets that make no groups, among them."""
+    import torch
+    g = np.random.default_rng(2840)
+    sizes = [0] * groups
+    sizes[1], sizes[-2] = 2, 3
+    cache = Shared(g, q, sizes, [20] * groups, [5] * 5, 2, 64, 16, 16, "bf16")
+    qt, _ = rand16(g, (5, 4, 64), "bf16")
+    clean = cache.call(q, qt)
+
+    def count(**more):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        return cache.call(q, qt, err_count=err, **more), int(err[0])
+
+    assert count()[1] == 0
+    cache.prefix_lens[0], cache.prefix_lens[-1] = -1, 2 ** 31 - 1  # of nobody
+    out, n = count()
+    assert n == 2 and torch.equal(out, clean)
+    cache.prefix_lens[1] = cache.prefix_table.shape[1] * 16 + 1  # of two sequences
+    cache.own_lens[4] = -7
+    assert count()[1] == 4
+    falling = cache.offsets.clone()
+    falling[-1] = 0
+    assert count(group_offsets=falling)[1] == 5
