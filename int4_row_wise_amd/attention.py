@@ -230,7 +230,8 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin
         _want("err_count", err_count, (1,), torch.int32, dev)
     index = INDEX_INT64 if wide else INDEX_INT32
     if pair_axes is None and norm:
-        _check("qemb_norm_rope", load_attention_library().qemb_norm_rope(
+        _check("qemb_norm_rope", _launch(
+            dev, load_attention_library().qemb_norm_rope,
             q.data_ptr(), k.data_ptr(), _ptr(v), n, hq, hkv, d, _DTYPES[dtype], qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
             positions.data_ptr(), index, cos_sin.data_ptr(), places, rot, int(interleaved),
             _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(slots),
@@ -288,7 +289,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offset
         _want("lse", lse, (n, hq), torch.float32, dev)
     if err_count is not None:
         _want("err_count", err_count, (1,), torch.int32, dev)
-    _check("qemb_prompt_attention", load_attention_library().qemb_prompt_attention(
+    _check("qemb_prompt_attention", _launch(
+        dev, load_attention_library().qemb_prompt_attention,
         q.data_ptr(), k.data_ptr(), v.data_ptr(), n, k.shape[0], batch, hq, k.shape[1], d, _DTYPES[dtype], qs[0], qs[1],
         ks[0], ks[1], vs[0], vs[1], q_offsets.data_ptr(), k_offsets.data_ptr(), max_q, window, sinks,
         d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse), _ptr(err_count), _raw_stream(dev)))
@@ -351,7 +353,8 @@ def decode_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
         _want("workspace", workspace, workspace.shape, torch.uint8, dev)
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check("qemb_decode_attention", L.qemb_decode_attention(
+    _check("qemb_decode_attention", _launch(
+        dev, L.qemb_decode_attention,
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages, size, bits, b, hq, hkv, d, _DTYPES[dtype],
         block_table.data_ptr(), width, seq_lens.data_ptr(), window, sinks, d ** -0.5 if scale is None else scale,
         _ptr(mass), mass_len, out.data_ptr(), _ptr(lse), _ptr(workspace), _ptr(err_count), _raw_stream(dev)))
@@ -479,7 +482,8 @@ def evict(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tenso
         _want("new_lens", new_lens, (b,), torch.int32, dev)
     if err_count is not None:
         _want("err_count", err_count, (1,), torch.int32, dev)
-    _check("qemb_evict", load_attention_library().qemb_evict(
+    _check("qemb_evict", _launch(
+        dev, load_attention_library().qemb_evict,
         k_pages.data_ptr(), v_pages.data_ptr(), pages, size, row * k_pages.element_size(), b, hkv,
         block_table.data_ptr(), width, seq_lens.data_ptr(), mass.data_ptr(), mass_len, keep, sinks,
         recent, new_k_pages.data_ptr(), new_v_pages.data_ptr(), new_pages, new_block_table.data_ptr(),

@@ -1,0 +1,96 @@
+"""Every call runs with its tensors' GPU as the current one (CPU only: the
+library and the tensors' place are stood in for, nothing is computed)."""
+from __future__ import annotations
+
+import contextlib
+
+import pytest
+import torch
+
+import int4_row_wise_amd as q
+from int4_row_wise_amd import attention, serving
+
+FAR = 2  # the tensors' GPU; the current one is 0
+
+
+class Far(torch.Tensor):
+    """A tensor that says that it is on GPU FAR."""
+    is_cuda = True
+
+    def get_device(self):
+        return FAR
+
+
+def far(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype).as_subclass(Far)
+
+
+def ints(*shape):
+    return far(*shape, dtype=torch.int32)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """(entry point, the GPU that is current) of every call that enqueues work."""
+    seen, current = [], [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        was, current[0] = current[0], index if isinstance(index, int) else index.index
+        yield
+        current[0] = was
+
+    class Library:
+        def __getattr__(self, name):
+            def entry(*args):
+                if name.endswith("_bytes"):
+                    return 64
+                seen.append((name, current[0]))
+                return 0
+            return entry
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for module in (attention, serving):
+        monkeypatch.setattr(module, "_lib", Library())
+        monkeypatch.setattr(module, "_raw_stream", lambda index: 0)
+    return seen
+
+
+def heads():
+    return far(5, 4, 64), far(5, 2, 64), far(5, 2, 64)
+
+
+def pool(n=6):
+    return far(n, 2, 16, 64), far(n, 2, 16, 64)
+
+
+def test_norm_rope(calls):
+    x, k, v = heads()
+    pages = pool()
+    table, slots = far(50, 64, dtype=torch.float32), far(5, dtype=torch.int64)
+    q.norm_rope(x, k, ints(5), table, k_out=far(5, 2, 64))
+    q.norm_rope(x, k, ints(5), table, v=v, k_pages=pages[0], v_pages=pages[1], slots=slots)
+    q.norm_rope(x, k, ints(5), table, norm=False, k_out=far(5, 2, 64))
+    q.norm_rope(x, k, ints(3, 5), table, pair_axes=far(32, dtype=torch.uint8), k_out=far(5, 2, 64))
+    assert calls == [("qemb_norm_rope", FAR)] * 2 + [("qemb_norm_rope_axes", FAR)] * 2
+
+
+def test_attention(calls):
+    x, k, v = heads()
+    pages = pool()
+    q.prompt_attention(x, k, v, ints(3), ints(3))
+    q.decode_attention(x, *pages, ints(5, 2), ints(5))
+    q.shared_attention(x, *pages, ints(1, 2), ints(1), ints(5, 2), ints(5))
+    assert calls == [(n, FAR) for n in ("qemb_prompt_attention", "qemb_decode_attention", "qemb_shared_attention")]
+
+
+def test_evict(calls):
+    q.evict(*pool(), ints(3, 2), ints(3), far(3, 2, 32, dtype=torch.float32), 16, *pool(), ints(3, 1))
+    assert calls == [("qemb_evict", FAR)]
+
+
+def test_serving(calls):
+    q.add_norm(far(4, 64), far(4, 64))
+    q.token_logprobs(far(4, 100), far(4, dtype=torch.int64), top=2)
+    assert calls == [("qemb_add_norm", FAR), ("qemb_token_logprobs", FAR)]
