@@ -19,7 +19,7 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from .qemb import INDEX_INT32, INDEX_INT64, QembError, _ptr
+from .qemb import INDEX_INT32, INDEX_INT64, QembError, _launch, _ptr
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqemb_attention.so")
@@ -88,14 +88,6 @@ def _check(fn: str, rc: int) -> None:
 # (1.9 us of a call that takes about ten).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _launch(dev: int, fn, *args) -> int:
-    """Calls fn(*args) with the tensors' GPU as the current one: kernels are launched there."""
-    if dev == torch._C._cuda_getDevice():
-        return fn(*args)
-    with torch.cuda.device(dev):
-        return fn(*args)
 
 
 def _device(name: str, t: torch.Tensor) -> int:

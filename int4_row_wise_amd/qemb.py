@@ -130,6 +130,14 @@ def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+def _launch(dev: int, fn, *args) -> int:
+    """Calls fn(*args) with the tensors' GPU as the current one: kernels are launched there."""
+    if dev == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _dev(name: str, t: torch.Tensor, dtype=None) -> None:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
@@ -171,7 +179,8 @@ def quantize_rowwise(x: torch.Tensor, bits: int = 4, clip_mode=RANGE, n_bins: in
     _dev("out", out, torch.uint8)
     if tuple(out.shape) != (rows, S):
         raise ValueError("out must be [%d, %d]" % (rows, S))
-    _check("qemb_quantize_rowwise", load_library().qemb_quantize_rowwise(
+    _check("qemb_quantize_rowwise", _launch(
+        x.get_device(), load_library().qemb_quantize_rowwise,
         _ptr(x), rows, dim, bits, _clip(clip_mode), n_bins, n_steps, _ptr(out), _stream(x)))
     return out
 
@@ -188,7 +197,8 @@ def quantize_baseline(x: torch.Tensor, bits: int = 4, method: int = SYMMETRIC, p
     _dev("out", out, torch.uint8)
     if tuple(out.shape) != (rows, S):
         raise ValueError("out must be [%d, %d]" % (rows, S))
-    _check("qemb_quantize_baseline", load_library().qemb_quantize_baseline(
+    _check("qemb_quantize_baseline", _launch(
+        x.get_device(), load_library().qemb_quantize_baseline,
         _ptr(x), rows, dim, bits, int(method), float(param), _ptr(out), _stream(x)))
     return out
 
@@ -203,7 +213,8 @@ def dequantize(packed: torch.Tensor, dim: int, bits: int = 4,
     if out is None:
         out = torch.empty((rows, dim), dtype=torch.float32, device=packed.device)
     _dev("out", out, torch.float32)
-    _check("qemb_dequantize", load_library().qemb_dequantize(
+    _check("qemb_dequantize", _launch(
+        packed.get_device(), load_library().qemb_dequantize,
         _ptr(packed), rows, dim, bits, _ptr(out), _stream(packed)))
     return out
 
@@ -259,7 +270,8 @@ def bag_forward(packed: torch.Tensor, table_offsets: torch.Tensor, B: int, dim: 
         packed, table_offsets, B, dim, indices, offsets, weights, pool_mode, out, err_count,
         total_rows)
     _check_rows(packed, row_stride(dim, bits), total_rows)
-    _check("qemb_bag_forward", load_library().qemb_bag_forward(
+    _check("qemb_bag_forward", _launch(
+        packed.get_device(), load_library().qemb_bag_forward,
         _ptr(packed), total_rows, _ptr(table_offsets), T, B, dim, bits, _ptr(indices),
         _ptr(offsets), indices.numel(), itype, pool_mode, _ptr(weights), _ptr(out),
         _ptr(err_count), _stream(packed)))
@@ -281,7 +293,8 @@ def l2_error(x: torch.Tensor, packed: torch.Tensor, bits: int,
         workspace = torch.empty(l2_error_workspace_bytes(), dtype=torch.uint8, device=x.device)
     if out4 is None:
         out4 = torch.empty(4, dtype=torch.float64, device=x.device)
-    _check("qemb_l2_error", load_library().qemb_l2_error(
+    _check("qemb_l2_error", _launch(
+        x.get_device(), load_library().qemb_l2_error,
         _ptr(x), _ptr(packed), rows, dim, bits, _ptr(workspace), _ptr(out4), _stream(x)))
     return _l2_dict(out4)
 
@@ -312,7 +325,8 @@ def quantize_codebook(x: torch.Tensor, n_iter: int = CODEBOOK_ITERS,
     _dev("out", out, torch.uint8)
     if tuple(out.shape) != (rows, S):
         raise ValueError("out must be [%d, %d]" % (rows, S))
-    _check("qemb_quantize_codebook", load_library().qemb_quantize_codebook(
+    _check("qemb_quantize_codebook", _launch(
+        x.get_device(), load_library().qemb_quantize_codebook,
         _ptr(x), rows, dim, n_iter, _ptr(out), _stream(x)))
     return out
 
@@ -327,7 +341,8 @@ def dequantize_codebook(packed: torch.Tensor, dim: int,
     if out is None:
         out = torch.empty((rows, dim), dtype=torch.float32, device=packed.device)
     _dev("out", out, torch.float32)
-    _check("qemb_dequantize_codebook", load_library().qemb_dequantize_codebook(
+    _check("qemb_dequantize_codebook", _launch(
+        packed.get_device(), load_library().qemb_dequantize_codebook,
         _ptr(packed), rows, dim, _ptr(out), _stream(packed)))
     return out
 
@@ -343,7 +358,8 @@ def bag_forward_codebook(packed: torch.Tensor, table_offsets: torch.Tensor, B: i
         packed, table_offsets, B, dim, indices, offsets, weights, pool_mode, out, err_count,
         total_rows)
     _check_rows(packed, codebook_row_stride(dim), total_rows)
-    _check("qemb_bag_forward_codebook", load_library().qemb_bag_forward_codebook(
+    _check("qemb_bag_forward_codebook", _launch(
+        packed.get_device(), load_library().qemb_bag_forward_codebook,
         _ptr(packed), total_rows, _ptr(table_offsets), T, B, dim, _ptr(indices), _ptr(offsets),
         indices.numel(), itype, pool_mode, _ptr(weights), _ptr(out), _ptr(err_count),
         _stream(packed)))
@@ -362,7 +378,8 @@ def l2_error_codebook(x: torch.Tensor, packed: torch.Tensor,
         workspace = torch.empty(l2_error_workspace_bytes(), dtype=torch.uint8, device=x.device)
     if out4 is None:
         out4 = torch.empty(4, dtype=torch.float64, device=x.device)
-    _check("qemb_l2_error_codebook", load_library().qemb_l2_error_codebook(
+    _check("qemb_l2_error_codebook", _launch(
+        x.get_device(), load_library().qemb_l2_error_codebook,
         _ptr(x), _ptr(packed), rows, dim, _ptr(workspace), _ptr(out4), _stream(x)))
     return _l2_dict(out4)
 
@@ -394,7 +411,8 @@ def dot_interaction(dense: torch.Tensor, pooled: torch.Tensor,
     _dev("out", out, torch.float32)
     if tuple(out.shape) != (B, W):
         raise ValueError("out must be [%d, %d]" % (B, W))
-    _check("qemb_dot_interaction", load_library().qemb_dot_interaction(
+    _check("qemb_dot_interaction", _launch(
+        dense.get_device(), load_library().qemb_dot_interaction,
         _ptr(dense), _ptr(pooled), B, T, dim, _ptr(out), _stream(dense)))
     return out
 
@@ -454,7 +472,8 @@ def compress_pooled(x: torch.Tensor, eb: torch.Tensor, T: Optional[int] = None,
     if out.numel() < compress_bound(n, dim) or offs.numel() != n + 1 or \
             workspace.numel() < compress_workspace_bytes(n):
         raise ValueError("out, offs or workspace too small")
-    _check("qemb_compress_pooled", load_library().qemb_compress_pooled(
+    _check("qemb_compress_pooled", _launch(
+        x.get_device(), load_library().qemb_compress_pooled,
         _ptr(x), n, dim, T, _ptr(eb), _ptr(out), _ptr(offs), _ptr(workspace), _stream(x)))
     return out, offs
 
@@ -477,7 +496,8 @@ def compress_pooled_noalloc(x: torch.Tensor, eb: torch.Tensor, out: torch.Tensor
         raise ValueError("eb must hold %d bounds" % T)
     if out.numel() < compress_bound(n, dim) or offs.numel() != n + 1:
         raise ValueError("out or offs too small")
-    _check("qemb_compress_pooled_noalloc", load_library().qemb_compress_pooled_noalloc(
+    _check("qemb_compress_pooled_noalloc", _launch(
+        x.get_device(), load_library().qemb_compress_pooled_noalloc,
         _ptr(x), n, dim, T, _ptr(eb), _ptr(out), _ptr(offs), _stream(x)))
     return out, offs
 
@@ -500,6 +520,7 @@ def decompress_pooled(buf: torch.Tensor, offs: torch.Tensor, dim: int, eb: torch
     nb = buf.numel() if in_bytes is None else int(in_bytes)
     if nb > buf.numel():
         raise ValueError("in_bytes exceeds the buffer")
-    _check("qemb_decompress_pooled", load_library().qemb_decompress_pooled(
+    _check("qemb_decompress_pooled", _launch(
+        buf.get_device(), load_library().qemb_decompress_pooled,
         _ptr(buf), nb, _ptr(offs), n, dim, eb.numel(), _ptr(eb), _ptr(y), _ptr(err_count), _stream(buf)))
     return y

@@ -94,3 +94,42 @@ def test_serving(calls):
     q.add_norm(far(4, 64), far(4, 64))
     q.token_logprobs(far(4, 100), far(4, dtype=torch.int64), top=2)
     assert calls == [("qemb_add_norm", FAR), ("qemb_token_logprobs", FAR)]
+
+
+@pytest.fixture
+def tables(calls, monkeypatch):
+    """The table library stood in for, too: a row of 64 elements has 48 bytes."""
+    from int4_row_wise_amd import qemb
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith("_stride"):
+                return lambda *args: 48
+            if name.endswith(("_bound", "_bytes", "_width")):
+                return lambda *args: 64
+            return getattr(attention._lib, name)
+
+    monkeypatch.setattr(qemb, "_lib", Library())
+    monkeypatch.setattr(qemb, "_stream", lambda t: 0)
+    return calls
+
+
+def test_tables(tables):
+    f32, u8, i64 = torch.float32, torch.uint8, torch.int64
+    x, rows = far(3, 64, dtype=f32), far(3, 48, dtype=u8)
+    q.quantize_rowwise(x, 4, out=rows)
+    q.quantize_baseline(x, 4, out=rows)
+    q.dequantize(rows, 64, 4, out=x)
+    q.quantize_codebook(x, out=rows)
+    q.dequantize_codebook(rows, 64, out=x)
+    ids, spans, pooled = far(4, dtype=i64), far(3, dtype=i64), far(2, 1, 64, dtype=f32)
+    q.bag_forward(rows, far(2, dtype=i64), 2, 64, 4, ids, spans, out=pooled)
+    q.bag_forward_codebook(rows, far(2, dtype=i64), 2, 64, ids, spans, out=pooled)
+    q.l2_error(x, rows, 4)
+    q.l2_error_codebook(x, rows)
+    q.dot_interaction(far(3, 64, dtype=f32), far(3, 2, 64, dtype=f32), out=far(3, 64, dtype=f32))
+    eb, offs, room = far(1, dtype=f32), far(4, dtype=i64), far(64, dtype=u8)
+    q.compress_pooled(x, eb, T=1, out=room, offs=offs, workspace=room)
+    q.compress_pooled_noalloc(x, eb, room, offs, T=1)
+    q.decompress_pooled(room, offs, 64, eb, y=x)
+    assert [place for _, place in tables] == [FAR] * 13 and len({name for name, _ in tables}) == 13
