@@ -147,6 +147,13 @@ def _dev(name: str, t: torch.Tensor, dtype=None) -> None:
         raise ValueError("%s must be contiguous" % name)
 
 
+def _room(name: str, t: torch.Tensor, dtype, count: int) -> None:
+    """A contiguous GPU array that holds at least what the kernels write to it."""
+    _dev(name, t, dtype)
+    if t.numel() < count:
+        raise ValueError("%s must hold at least %d elements, got %d" % (name, count, t.numel()))
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -212,7 +219,7 @@ def dequantize(packed: torch.Tensor, dim: int, bits: int = 4,
         raise ValueError("packed must be [rows, %d]" % row_stride(dim, bits))
     if out is None:
         out = torch.empty((rows, dim), dtype=torch.float32, device=packed.device)
-    _dev("out", out, torch.float32)
+    _room("out", out, torch.float32, rows * dim)
     _check("qemb_dequantize", _launch(
         packed.get_device(), load_library().qemb_dequantize,
         _ptr(packed), rows, dim, bits, _ptr(out), _stream(packed)))
@@ -242,9 +249,9 @@ def _bag_args(packed, table_offsets, B, dim, indices, offsets, weights, pool_mod
             raise ValueError("weights must match indices")
     if out is None:
         out = torch.empty((B, T, dim), dtype=torch.float32, device=packed.device)
-    _dev("out", out, torch.float32)
+    _room("out", out, torch.float32, B * T * dim)
     if err_count is not None:
-        _dev("err_count", err_count, torch.int32)
+        _room("err_count", err_count, torch.int32, 1)
     if total_rows is None:
         total_rows = packed.shape[0]
     return T, itype, pool_mode, out, total_rows
@@ -291,8 +298,12 @@ def l2_error(x: torch.Tensor, packed: torch.Tensor, bits: int,
     _check_rows(packed, row_stride(dim, bits), rows)
     if workspace is None:
         workspace = torch.empty(l2_error_workspace_bytes(), dtype=torch.uint8, device=x.device)
+    else:
+        _room("workspace", workspace, torch.uint8, l2_error_workspace_bytes())
     if out4 is None:
         out4 = torch.empty(4, dtype=torch.float64, device=x.device)
+    else:
+        _room("out4", out4, torch.float64, 4)
     _check("qemb_l2_error", _launch(
         x.get_device(), load_library().qemb_l2_error,
         _ptr(x), _ptr(packed), rows, dim, bits, _ptr(workspace), _ptr(out4), _stream(x)))
@@ -340,7 +351,7 @@ def dequantize_codebook(packed: torch.Tensor, dim: int,
         raise ValueError("packed must be [rows, %d]" % codebook_row_stride(dim))
     if out is None:
         out = torch.empty((rows, dim), dtype=torch.float32, device=packed.device)
-    _dev("out", out, torch.float32)
+    _room("out", out, torch.float32, rows * dim)
     _check("qemb_dequantize_codebook", _launch(
         packed.get_device(), load_library().qemb_dequantize_codebook,
         _ptr(packed), rows, dim, _ptr(out), _stream(packed)))
@@ -376,8 +387,12 @@ def l2_error_codebook(x: torch.Tensor, packed: torch.Tensor,
     _check_rows(packed, codebook_row_stride(dim), rows)
     if workspace is None:
         workspace = torch.empty(l2_error_workspace_bytes(), dtype=torch.uint8, device=x.device)
+    else:
+        _room("workspace", workspace, torch.uint8, l2_error_workspace_bytes())
     if out4 is None:
         out4 = torch.empty(4, dtype=torch.float64, device=x.device)
+    else:
+        _room("out4", out4, torch.float64, 4)
     _check("qemb_l2_error_codebook", _launch(
         x.get_device(), load_library().qemb_l2_error_codebook,
         _ptr(x), _ptr(packed), rows, dim, _ptr(workspace), _ptr(out4), _stream(x)))
@@ -517,6 +532,8 @@ def decompress_pooled(buf: torch.Tensor, offs: torch.Tensor, dim: int, eb: torch
     _dev("y", y, torch.float32)
     if y.numel() != max(n, 0) * dim:
         raise ValueError("y must hold %d x %d values" % (n, dim))
+    if err_count is not None:
+        _room("err_count", err_count, torch.int32, 1)
     nb = buf.numel() if in_bytes is None else int(in_bytes)
     if nb > buf.numel():
         raise ValueError("in_bytes exceeds the buffer")

@@ -133,3 +133,27 @@ def test_tables(tables):
     q.compress_pooled_noalloc(x, eb, room, offs, T=1)
     q.decompress_pooled(room, offs, 64, eb, y=x)
     assert [place for _, place in tables] == [FAR] * 13 and len({name for name, _ in tables}) == 13
+
+
+def test_tables_refuse_arrays_too_small(tables):
+    """What a kernel would write past is refused before anything is enqueued."""
+    f32, u8, i32, i64 = torch.float32, torch.uint8, torch.int32, torch.int64
+    x, rows, small = far(3, 64, dtype=f32), far(3, 48, dtype=u8), far(2, 64, dtype=f32)
+    bag = (far(2, dtype=i64), 4, 64)
+    ids, spans = far(4, dtype=i64), far(5, dtype=i64)
+    none, offs, eb = far(0, dtype=i32), far(4, dtype=i64), far(1, dtype=f32)
+    for call in (
+        lambda: q.dequantize(rows, 64, 4, out=small),
+        lambda: q.dequantize_codebook(rows, 64, out=small),
+        lambda: q.bag_forward(rows, *bag, 4, ids, spans, out=x),
+        lambda: q.bag_forward(rows, *bag, 4, ids, spans, out=far(4, 1, 64, dtype=f32), err_count=none),
+        lambda: q.bag_forward_codebook(rows, *bag, ids, spans, out=x),
+        lambda: q.l2_error(x, rows, 4, workspace=far(63, dtype=u8)),
+        lambda: q.l2_error(x, rows, 4, out4=far(3, dtype=torch.float64)),
+        lambda: q.l2_error_codebook(x, rows, workspace=far(63, dtype=u8)),
+        lambda: q.l2_error_codebook(x, rows, out4=far(3, dtype=torch.float64)),
+        lambda: q.decompress_pooled(far(64, dtype=u8), offs, 64, eb, y=x, err_count=none),
+    ):
+        with pytest.raises(ValueError):
+            call()
+    assert tables == []
