@@ -212,3 +212,41 @@ def test_captured_replays(q):
         torch.cuda.synchronize()
         for a, w in zip(res, step(x.clone(), pos.clone())):
             assert torch.equal(a, w), rep
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("d,rot,norm", [(16, 16, True), (64, 32, False), (96, 96, True), (128, 128, True), (128, 64, False), (256, 256, False)])
+def test_append_of_unequal_positions(q, d, rot, norm, bits, interleaved):
+    """Keys turned by another position on each axis, in every row format, against float64."""
+    import torch
+    g = np.random.default_rng(3500 + d + bits)
+    n, hkv, page, pages, eps = 57, 3, 8, 9, 1e-5
+    (qt, _), (kt, kv), (vt, vv) = (rand16(g, (n, h, d), "bf16", 1.5) for h in (2, hkv, hkv))
+    wk, wkv = rand16(g, (d,), "bf16")
+    table = rope_table(90, rot)
+    pos, axis = g.integers(0, 90, (3, n)), g.integers(0, 4, rot // 2)  # some pairs of no axis
+    slots = g.permutation(pages * page)[:n]
+    row = d if bits == 16 else q.row_stride(d, bits)
+    pool = [torch.full((pages, hkv, page, row), 77, dtype=torch.bfloat16 if bits == 16 else torch.uint8, device="cuda") for _ in range(2)]
+    q.norm_rope(qt, kt, torch.from_numpy(pos).cuda(), torch.from_numpy(table).cuda(), None, wk if norm else None, eps=eps, interleaved=interleaved,
+                v=vt, k_pages=pool[0], v_pages=pool[1], slots=torch.from_numpy(slots).cuda(), bits=bits, norm=norm,
+                pair_axes=torch.from_numpy(axis.astype(np.uint8)).cuda())
+    cos, sin = angles(table, pos, axis)
+    want_k = expected(kv, wkv, cos, sin, eps, interleaved, norm)
+    for p, want, own in ((pool[0], want_k, bound(want_k, kv, wkv, eps, "bf16", d, norm)), (pool[1], vv, np.zeros_like(vv))):
+        rows = host(p.view(torch.uint8)).transpose(0, 2, 1, 3).reshape(pages * page, hkv, -1)
+        free = np.ones(pages * page, bool)
+        free[slots] = False
+        if bits == 16:
+            close(f64(p).transpose(0, 2, 1, 3).reshape(pages * page, hkv, d)[slots], want, own, "rows")
+            continue
+        assert (rows[free] == 77).all()
+        values, rng = model.unpack_rows(rows[slots], d, bits)
+        # The packed value is off from the row by half a step, by what binary16 rounds of scale (times the last
+        # code) and bias, half an ulp each (2^-11; 2^-25 below its normal range, the scale's times 255), and by
+        # binary32 before, which `own` holds (its 16-bit rounding is not made here)
+        most = np.abs(want).max(-1, keepdims=True)
+        step = rng[..., None] / (2 ** bits - 1)
+        limit = 0.5 * step * (1 + 2.0 ** -9) + 2.0 ** -11 * (rng[..., None] + most) + 2.0 ** -25 * 256 + own
+        close(values, want, np.broadcast_to(limit, want.shape), "packed rows")
