@@ -3,8 +3,9 @@ stands around the attention in a serving loop, the residual's addition with a
 norm and the log probabilities of tokens.
 
 Argument marshalling only: the kernels run behind the C ABI, on the current
-stream, and nothing synchronizes.  Outputs and workspaces are torch tensors,
-allocated here unless given.
+stream of the tensors' GPU, and nothing synchronizes.  Outputs and workspaces are
+torch tensors, allocated here where none can be or is given (token_logprobs takes
+lse and a workspace; its other outputs are new ones).
 """
 from __future__ import annotations
 
