@@ -147,6 +147,14 @@ def _dev(name: str, t: torch.Tensor, dtype=None) -> None:
         raise ValueError("%s must be contiguous" % name)
 
 
+def _place(*tensors: Optional[torch.Tensor]) -> int:
+    """The GPU index that all tensors of a call share (None: not given)."""
+    places = {t.get_device() for t in tensors if t is not None}
+    if len(places) != 1:
+        raise ValueError("all tensors must be on one GPU, got %s" % sorted(places))
+    return places.pop()
+
+
 def _room(name: str, t: torch.Tensor, dtype, count: int) -> None:
     """A contiguous GPU array that holds at least what the kernels write to it."""
     _dev(name, t, dtype)
@@ -187,7 +195,7 @@ def quantize_rowwise(x: torch.Tensor, bits: int = 4, clip_mode=RANGE, n_bins: in
     if tuple(out.shape) != (rows, S):
         raise ValueError("out must be [%d, %d]" % (rows, S))
     _check("qemb_quantize_rowwise", _launch(
-        x.get_device(), load_library().qemb_quantize_rowwise,
+        _place(x, out), load_library().qemb_quantize_rowwise,
         _ptr(x), rows, dim, bits, _clip(clip_mode), n_bins, n_steps, _ptr(out), _stream(x)))
     return out
 
@@ -205,7 +213,7 @@ def quantize_baseline(x: torch.Tensor, bits: int = 4, method: int = SYMMETRIC, p
     if tuple(out.shape) != (rows, S):
         raise ValueError("out must be [%d, %d]" % (rows, S))
     _check("qemb_quantize_baseline", _launch(
-        x.get_device(), load_library().qemb_quantize_baseline,
+        _place(x, out), load_library().qemb_quantize_baseline,
         _ptr(x), rows, dim, bits, int(method), float(param), _ptr(out), _stream(x)))
     return out
 
@@ -221,7 +229,7 @@ def dequantize(packed: torch.Tensor, dim: int, bits: int = 4,
         out = torch.empty((rows, dim), dtype=torch.float32, device=packed.device)
     _room("out", out, torch.float32, rows * dim)
     _check("qemb_dequantize", _launch(
-        packed.get_device(), load_library().qemb_dequantize,
+        _place(packed, out), load_library().qemb_dequantize,
         _ptr(packed), rows, dim, bits, _ptr(out), _stream(packed)))
     return out
 
@@ -278,7 +286,7 @@ def bag_forward(packed: torch.Tensor, table_offsets: torch.Tensor, B: int, dim: 
         total_rows)
     _check_rows(packed, row_stride(dim, bits), total_rows)
     _check("qemb_bag_forward", _launch(
-        packed.get_device(), load_library().qemb_bag_forward,
+        _place(packed, table_offsets, indices, offsets, weights, out, err_count), load_library().qemb_bag_forward,
         _ptr(packed), total_rows, _ptr(table_offsets), T, B, dim, bits, _ptr(indices),
         _ptr(offsets), indices.numel(), itype, pool_mode, _ptr(weights), _ptr(out),
         _ptr(err_count), _stream(packed)))
@@ -305,7 +313,7 @@ def l2_error(x: torch.Tensor, packed: torch.Tensor, bits: int,
     else:
         _room("out4", out4, torch.float64, 4)
     _check("qemb_l2_error", _launch(
-        x.get_device(), load_library().qemb_l2_error,
+        _place(x, packed, workspace, out4), load_library().qemb_l2_error,
         _ptr(x), _ptr(packed), rows, dim, bits, _ptr(workspace), _ptr(out4), _stream(x)))
     return _l2_dict(out4)
 
@@ -337,7 +345,7 @@ def quantize_codebook(x: torch.Tensor, n_iter: int = CODEBOOK_ITERS,
     if tuple(out.shape) != (rows, S):
         raise ValueError("out must be [%d, %d]" % (rows, S))
     _check("qemb_quantize_codebook", _launch(
-        x.get_device(), load_library().qemb_quantize_codebook,
+        _place(x, out), load_library().qemb_quantize_codebook,
         _ptr(x), rows, dim, n_iter, _ptr(out), _stream(x)))
     return out
 
@@ -353,7 +361,7 @@ def dequantize_codebook(packed: torch.Tensor, dim: int,
         out = torch.empty((rows, dim), dtype=torch.float32, device=packed.device)
     _room("out", out, torch.float32, rows * dim)
     _check("qemb_dequantize_codebook", _launch(
-        packed.get_device(), load_library().qemb_dequantize_codebook,
+        _place(packed, out), load_library().qemb_dequantize_codebook,
         _ptr(packed), rows, dim, _ptr(out), _stream(packed)))
     return out
 
@@ -370,7 +378,7 @@ def bag_forward_codebook(packed: torch.Tensor, table_offsets: torch.Tensor, B: i
         total_rows)
     _check_rows(packed, codebook_row_stride(dim), total_rows)
     _check("qemb_bag_forward_codebook", _launch(
-        packed.get_device(), load_library().qemb_bag_forward_codebook,
+        _place(packed, table_offsets, indices, offsets, weights, out, err_count), load_library().qemb_bag_forward_codebook,
         _ptr(packed), total_rows, _ptr(table_offsets), T, B, dim, _ptr(indices), _ptr(offsets),
         indices.numel(), itype, pool_mode, _ptr(weights), _ptr(out), _ptr(err_count),
         _stream(packed)))
@@ -394,7 +402,7 @@ def l2_error_codebook(x: torch.Tensor, packed: torch.Tensor,
     else:
         _room("out4", out4, torch.float64, 4)
     _check("qemb_l2_error_codebook", _launch(
-        x.get_device(), load_library().qemb_l2_error_codebook,
+        _place(x, packed, workspace, out4), load_library().qemb_l2_error_codebook,
         _ptr(x), _ptr(packed), rows, dim, _ptr(workspace), _ptr(out4), _stream(x)))
     return _l2_dict(out4)
 
@@ -427,7 +435,7 @@ def dot_interaction(dense: torch.Tensor, pooled: torch.Tensor,
     if tuple(out.shape) != (B, W):
         raise ValueError("out must be [%d, %d]" % (B, W))
     _check("qemb_dot_interaction", _launch(
-        dense.get_device(), load_library().qemb_dot_interaction,
+        _place(dense, pooled, out), load_library().qemb_dot_interaction,
         _ptr(dense), _ptr(pooled), B, T, dim, _ptr(out), _stream(dense)))
     return out
 
@@ -488,7 +496,7 @@ def compress_pooled(x: torch.Tensor, eb: torch.Tensor, T: Optional[int] = None,
             workspace.numel() < compress_workspace_bytes(n):
         raise ValueError("out, offs or workspace too small")
     _check("qemb_compress_pooled", _launch(
-        x.get_device(), load_library().qemb_compress_pooled,
+        _place(x, eb, out, offs, workspace), load_library().qemb_compress_pooled,
         _ptr(x), n, dim, T, _ptr(eb), _ptr(out), _ptr(offs), _ptr(workspace), _stream(x)))
     return out, offs
 
@@ -512,7 +520,7 @@ def compress_pooled_noalloc(x: torch.Tensor, eb: torch.Tensor, out: torch.Tensor
     if out.numel() < compress_bound(n, dim) or offs.numel() != n + 1:
         raise ValueError("out or offs too small")
     _check("qemb_compress_pooled_noalloc", _launch(
-        x.get_device(), load_library().qemb_compress_pooled_noalloc,
+        _place(x, eb, out, offs), load_library().qemb_compress_pooled_noalloc,
         _ptr(x), n, dim, T, _ptr(eb), _ptr(out), _ptr(offs), _stream(x)))
     return out, offs
 
@@ -538,6 +546,6 @@ def decompress_pooled(buf: torch.Tensor, offs: torch.Tensor, dim: int, eb: torch
     if nb > buf.numel():
         raise ValueError("in_bytes exceeds the buffer")
     _check("qemb_decompress_pooled", _launch(
-        buf.get_device(), load_library().qemb_decompress_pooled,
+        _place(buf, offs, eb, y, err_count), load_library().qemb_decompress_pooled,
         _ptr(buf), nb, _ptr(offs), n, dim, eb.numel(), _ptr(eb), _ptr(y), _ptr(err_count), _stream(buf)))
     return y

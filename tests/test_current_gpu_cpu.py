@@ -125,8 +125,9 @@ def test_tables(tables):
     ids, spans, pooled = far(4, dtype=i64), far(3, dtype=i64), far(2, 1, 64, dtype=f32)
     q.bag_forward(rows, far(2, dtype=i64), 2, 64, 4, ids, spans, out=pooled)
     q.bag_forward_codebook(rows, far(2, dtype=i64), 2, 64, ids, spans, out=pooled)
-    q.l2_error(x, rows, 4)
-    q.l2_error_codebook(x, rows)
+    room4 = dict(workspace=far(64, dtype=u8), out4=far(4, dtype=torch.float64))
+    q.l2_error(x, rows, 4, **room4)
+    q.l2_error_codebook(x, rows, **room4)
     q.dot_interaction(far(3, 64, dtype=f32), far(3, 2, 64, dtype=f32), out=far(3, 64, dtype=f32))
     eb, offs, room = far(1, dtype=f32), far(4, dtype=i64), far(64, dtype=u8)
     q.compress_pooled(x, eb, T=1, out=room, offs=offs, workspace=room)
@@ -153,6 +154,43 @@ def test_tables_refuse_arrays_too_small(tables):
         lambda: q.l2_error_codebook(x, rows, workspace=far(63, dtype=u8)),
         lambda: q.l2_error_codebook(x, rows, out4=far(3, dtype=torch.float64)),
         lambda: q.decompress_pooled(far(64, dtype=u8), offs, 64, eb, y=x, err_count=none),
+    ):
+        with pytest.raises(ValueError):
+            call()
+    assert tables == []
+
+
+def test_tables_refuse_tensors_of_several_gpus(tables):
+    f32, u8, i64 = torch.float32, torch.uint8, torch.int64
+
+    class Elsewhere(Far):
+        def get_device(self):
+            return FAR + 1
+
+    def other(*shape, dtype):
+        return torch.zeros(shape, dtype=dtype).as_subclass(Elsewhere)
+
+    x, rows = far(3, 64, dtype=f32), far(3, 48, dtype=u8)
+    ids, spans, pooled = far(4, dtype=i64), far(3, dtype=i64), far(2, 1, 64, dtype=f32)
+    eb, offs, room = far(1, dtype=f32), far(4, dtype=i64), far(64, dtype=u8)
+    bag = dict(B=2, dim=64, indices=ids, offsets=spans, out=pooled)
+    for call in (
+        lambda: q.quantize_rowwise(x, 4, out=other(3, 48, dtype=u8)),
+        lambda: q.quantize_baseline(x, 4, out=other(3, 48, dtype=u8)),
+        lambda: q.dequantize(rows, 64, 4, out=other(3, 64, dtype=f32)),
+        lambda: q.quantize_codebook(x, out=other(3, 48, dtype=u8)),
+        lambda: q.dequantize_codebook(rows, 64, out=other(3, 64, dtype=f32)),
+        lambda: q.bag_forward(rows, other(2, dtype=i64), bits=4, **bag),
+        lambda: q.bag_forward(rows, far(2, dtype=i64), bits=4, **bag | dict(indices=other(4, dtype=i64))),
+        lambda: q.bag_forward(rows, far(2, dtype=i64), bits=4, weights=other(4, dtype=f32), **bag),
+        lambda: q.bag_forward(rows, far(2, dtype=i64), bits=4, err_count=other(1, dtype=torch.int32), **bag),
+        lambda: q.bag_forward_codebook(rows, far(2, dtype=i64), **bag | dict(offsets=other(3, dtype=i64))),
+        lambda: q.l2_error(x, other(3, 48, dtype=u8), 4),
+        lambda: q.l2_error_codebook(x, other(3, 48, dtype=u8)),
+        lambda: q.dot_interaction(far(3, 64, dtype=f32), other(3, 2, 64, dtype=f32), out=far(3, 64, dtype=f32)),
+        lambda: q.compress_pooled(x, other(1, dtype=f32), T=1, out=room, offs=offs, workspace=room),
+        lambda: q.compress_pooled_noalloc(x, eb, room, other(4, dtype=i64), T=1),
+        lambda: q.decompress_pooled(room, offs, 64, eb, y=other(3, 64, dtype=f32)),
     ):
         with pytest.raises(ValueError):
             call()
