@@ -19,7 +19,7 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from .qemb import INDEX_INT32, INDEX_INT64, QembError, _launch, _ptr
+from .qemb import INDEX_INT32, INDEX_INT64, QembError, _launch, _ptr, _raw_stream
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqemb_attention.so")
@@ -82,12 +82,6 @@ def load_attention_library(path: str = LIB_PATH) -> ctypes.CDLL:
 def _check(fn: str, rc: int) -> None:
     if rc != 0:
         raise QembError(fn, rc, _REASONS.get(rc, "unknown error"))
-
-
-# The current stream's handle by device index, without building a Stream object
-# (1.9 us of a call that takes about ten).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _device(name: str, t: torch.Tensor) -> int:

@@ -15,8 +15,8 @@ from typing import Optional, Tuple
 
 import torch
 
-from .attention import _check, _device, _raw_stream, _want
-from .qemb import INDEX_INT32, INDEX_INT64, QembError, _launch, _ptr
+from .attention import _check, _device, _want
+from .qemb import INDEX_INT32, INDEX_INT64, QembError, _launch, _ptr, _raw_stream
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqemb_serving.so")
