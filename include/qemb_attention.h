@@ -35,7 +35,8 @@
  * 16-bit type, and over packed rows weight times scale to binary16 (and the
  * query, scaled to a largest element of 1 to 2, too: to at most 2^-25), so that
  * an output is off by up to that rounding of its weights and its own.  The
- * scale of the scores is finite, of any sign.
+ * scale of the scores is finite, its product with log2 e in binary32 too, of any
+ * sign.
  *
  * Conventions (those of qemb.h): every array is a device pointer owned by
  * the caller; nothing is allocated, kept or synchronized; work goes onto

@@ -57,6 +57,9 @@ inline bool strides_fit(int64_t token, int64_t head) {
   return token >= 0 && head >= 0 && token % 8 == 0 && head % 8 == 0;
 }
 
+// Scores are taken as powers of two.
+inline bool scale_fits(float scale) { return isfinite(scale * 1.44269504088896340736f); }
+
 // A stride along one token or one head is never taken, so it may be anything.
 inline int64_t taken(int64_t stride, int64_t count, int32_t dim) { return count > 1 ? stride : dim; }
 
@@ -151,7 +154,7 @@ int qemb_prompt_attention(const void* q, const void* k, const void* v, int64_t q
                           int64_t max_q, int32_t window, int32_t sinks, float scale, void* out,
                           float* lse, int32_t* err_count, qemb_stream_t stream) {
   if (q_tokens < 0 || k_tokens < 0 || batch < 0 || window < 0 || sinks < 0 || max_q < 0) return QEMB_E_INVALID_ARG;
-  if (!isfinite(scale)) return QEMB_E_INVALID_ARG;
+  if (!scale_fits(scale)) return QEMB_E_INVALID_ARG;
   if (q_tokens > kMostPlaces || k_tokens > kMostPlaces) return QEMB_E_UNSUPPORTED;
   if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
   q_token_stride = taken(q_token_stride, q_tokens, dim), q_head_stride = taken(q_head_stride, q_heads, dim);
@@ -199,7 +202,7 @@ int qemb_decode_attention(const void* q, const void* k_pages, const void* v_page
                           float scale, float* mass, int64_t mass_len, void* out, float* lse,
                           void* workspace, int32_t* err_count, qemb_stream_t stream) {
   if (batch < 0 || width < 0 || pages < 0 || window < 0 || sinks < 0 || !is_pow2(page_size)) return QEMB_E_INVALID_ARG;
-  if (!isfinite(scale)) return QEMB_E_INVALID_ARG;
+  if (!scale_fits(scale)) return QEMB_E_INVALID_ARG;
   if (bits != 16 && bits != 8 && bits != 4) return QEMB_E_INVALID_ARG;
   if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
   if ((int64_t)width * page_size > kMostPlaces) return QEMB_E_UNSUPPORTED;
@@ -244,7 +247,7 @@ int qemb_shared_attention(const void* q, const void* k_pages, const void* v_page
                           const int32_t* seq_lens, float scale, void* out, float* lse, void* workspace,
                           int32_t* err_count, qemb_stream_t stream) {
   if (batch < 0 || width < 0 || prefix_width < 0 || pages < 0 || groups < 1 || !is_pow2(page_size)) return QEMB_E_INVALID_ARG;
-  if (!isfinite(scale) || (groups > 1 && !group_offsets)) return QEMB_E_INVALID_ARG;
+  if (!scale_fits(scale) || (groups > 1 && !group_offsets)) return QEMB_E_INVALID_ARG;
   if (bits != 16 && bits != 8 && bits != 4) return QEMB_E_INVALID_ARG;
   if (int rc = check_groups(q_heads, kv_heads, dim, dtype)) return rc;
   if ((int64_t)width * page_size > kMostPlaces || (int64_t)prefix_width * page_size > kMostPlaces) return QEMB_E_UNSUPPORTED;

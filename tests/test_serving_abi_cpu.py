@@ -158,3 +158,12 @@ def test_launches_make_the_tensors_gpu_current(monkeypatch):
     monkeypatch.setattr(torch.cuda, "device", device)
     assert attention._launch(0, lambda *a: sum(a), 1, 2) == 3 and entered == []
     assert attention._launch(2, lambda *a: sum(a), 1, 2) == 3 and entered == [2]
+
+
+@pytest.mark.parametrize("scale,rc", [(3e38, -1), (-3e38, -1), (2.36e38, -1), (2.35e38, 0), (-2.35e38, 0), (0.0, 0), (1e-45, 0)])
+def test_scales_whose_powers_of_two_overflow_are_refused(attention_lib, scale, rc):  # noqa: F811
+    """Scores are taken as powers of two: a scale times log2 e past binary32 would make even scores of 0 a NaN."""
+    from tests.test_attention_abi_cpu import DECODE, PROMPT
+    assert call(attention_lib.qemb_prompt_attention, PROMPT, scale=scale, batch=0) == rc
+    assert call(attention_lib.qemb_decode_attention, DECODE, scale=scale, batch=0) == rc
+    assert call(attention_lib.qemb_shared_attention, SHARED, scale=scale, batch=0) == rc
